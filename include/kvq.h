@@ -246,7 +246,8 @@ KVQ_API int kvq_reset_sequences(kvq_handle *h, const int32_t *seqs, int n);
 
 
 /* Read and clear the device status word (synchronizes `stream`).  KVQ_EDEVICE if a
- * kernel reported a bounded wait that expired; *flags gets the raw bits. */
+ * kernel reported a bounded wait that expired (bit 0) or a slot index outside its source
+ * (bit 1, kvq_append_selected); *flags gets the raw bits. */
 KVQ_API int kvq_device_status(kvq_handle *h, void *stream, unsigned *flags);
 
 /* Decode attention without any caller-provided scratch: the same computation and
@@ -327,6 +328,92 @@ KVQ_API int kvq_tag_distortion_device(int num_layers, int num_requests, int n_q_
  * chosen sum.  Errors: KVQ_EINVAL (avg_bits outside [2, 4], negative counts, null). */
 KVQ_API int kvq_tag_allocate(int num_tags, const double *D2, const double *D4, const int64_t *counts,
                              double avg_bits, int *bits, double *total_distortion);
+
+/* ---- Steps of several tokens, score shapes, and reading the cache back (per-layer plans;
+ * paged plans: KVQ_EUNSUPPORTED) ------------------------------------------------------
+ * A step that verifies drafted tokens, or feeds a prompt in chunks, runs
+ *   kvq_norm_rope -> kvq_tree_attn -> (the caller accepts tokens) -> kvq_append_selected
+ * per layer.  The pages describe none of these; they are this library's own additions
+ * around the pages' cache. */
+
+/* Norm and rotation of a projection's rows. */
+typedef struct {
+    int rot_dim;           /* rotated channels of a head: 0 (none) .. head_dim, multiple of 16 */
+    int interleaved;       /* pairs (i, i + rot_dim / 2), or, if nonzero, (2i, 2i + 1) */
+    const float *inv_freq; /* device fp32 [rot_dim / 2]: pair i turns by position * inv_freq[i] */
+    const float *q_weight; /* device fp32 [head_dim] RMS-norm weight of query heads, or NULL: no norm */
+    const float *k_weight; /* the same for key heads */
+    float eps;             /* of the norm: x / sqrt(mean(x^2) + eps) * weight */
+} kvq_rope_desc;
+
+/* RMS norm of every query and key head, rotation by position, and the split of the rows
+ * into the layouts of kvq_append and kvq_tree_attn, in one launch.  qkv (device, bf16): the
+ * row of token i of request b starts at element b * batch_stride + i * token_stride and
+ * holds n_q_heads, then n_kv_heads key, then n_kv_heads value heads of head_dim channels.
+ * Its position is the layer's current length of request b plus offset[b * n + i] (device
+ * int32; NULL: plus i).  Writes q [B][n][Hq][D], K, V [B][Hkv][n][D] (bf16); V rows are
+ * copied unchanged.  Norm and rotation are computed in fp32 (the angle in fp64: exact for
+ * far positions) and rounded once.  Strides are multiples of 8 elements, token_stride at
+ * least (Hq + 2 Hkv) D, batch_stride >= 0; all pointers 16-byte aligned (offset, inv_freq
+ * and weights 4).  n >= 1.  No cache data is read or written. */
+KVQ_API int kvq_norm_rope(kvq_handle *h, int layer, const void *qkv, int64_t batch_stride, int64_t token_stride,
+                          int n, const int32_t *offset, const kvq_rope_desc *rope, void *q, void *K, void *V,
+                          void *stream);
+
+/* How scores become weights: s = scale * (q . k); capped s = softcap * tanh(s / softcap);
+ * then s -= alibi[hq] * (position of q - position of k); a key is seen only if position of
+ * q - position of k < window.  All-zero (or a NULL pointer to it): plain attention. */
+typedef struct {
+    float softcap;         /* 0: none; else > 0 */
+    const float *alibi;    /* device fp32 [n_q_heads], or NULL */
+    int window;            /* 0: none; else >= 1 */
+    float scale;           /* 0: 1 / sqrt(head_dim) */
+} kvq_score_opts;
+
+/* Attention of T drafted tokens per request over the packed cache of `layer` and over one
+ * another: q [B][T][Hq][D], K, V [B][Hkv][T][D] (device, bf16; not yet appended), out
+ * [B][T][Hq][D] bf16, or fp32 if out_fp32.  Every cached token is visible to every drafted
+ * token (up to opts' window); drafted token j is visible to token t if bit j % 32 of word
+ * j / 32 of mask row [b][t] is set (device uint32 [B][T][ceil(T / 32)]; a tree's rows hold
+ * the token's ancestors and itself, but any mask is allowed), or, mask NULL, if j <= t (a
+ * causal chunk).  Token t's position is the request's length + depth[b][t] (device int32
+ * [B][T]; NULL: t); positions only matter to opts.  n_draft (host int32 [B], in [0, T];
+ * NULL: T each): request b has its first n_draft[b] tokens; output rows from there on are
+ * left as they were, and the values behind them in q, K, V and mask have no influence.
+ * Requests may be empty (length 0).  A row that sees no key comes out as zeros; a key that
+ * a row does not see has no influence on it, whatever K and V hold there.  Cached and
+ * drafted values are taken as fp16 where they enter the second product (drafted values
+ * beyond its range saturate, as they would in the cache, unless infinite); scores,
+ * softmax and sums are fp32.  T <= 4096.  workspace: device memory of
+ * kvq_tree_attn_workspace_bytes, 256-byte aligned, owned by the call until it has run.
+ * One launch, and a merge launch when the sequence is split. */
+KVQ_API int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const void *V, int T,
+                          const int32_t *n_draft, const uint32_t *mask, const int32_t *depth,
+                          const kvq_score_opts *opts, void *out, int out_fp32, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of kvq_tree_attn for T drafted tokens at any cached length. */
+KVQ_API int kvq_tree_attn_workspace_bytes(const kvq_handle *h, int T, size_t *bytes);
+
+/* kvq_decode_attn with opts: one query token per request (q, out [B][Hq][D]) over all
+ * cached tokens of `layer`; the query's position is that of the last cached token.  Split
+ * partials live in the bound workspace.  Every request must hold a token. */
+KVQ_API int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_score_opts *opts, void *out,
+                                   int out_fp32, void *stream);
+
+/* kvq_append_ragged with the tokens picked by index: K, V [B][Hkv][n_src][D] (device), and
+ * request b appends its slots index[b * n_max + i], i < n_new[b], in that order (index:
+ * device int32 [B][n_max]; n_new: host int32 [B] in [0, n_max], NULL: n_max each).  A slot
+ * may be picked more than once.  A slot outside [0, n_src) is reported by
+ * kvq_device_status (KVQ_EDEVICE) and slot 0 is appended in its place. */
+KVQ_API int kvq_append_selected(kvq_handle *h, int layer, const void *K, const void *V, int n_src,
+                                const int32_t *index, const int32_t *n_new, int n_max, void *stream);
+
+/* Tokens [t0, t0 + n) of `layer` as the values the cache stands for, code * scale + zero
+ * rounded to bf16 (the open key group's bf16 keys as they are): K, V [B][Hkv][n][D] (device;
+ * either may be NULL).  Requests shorter than t0 + n leave the rows behind their last token
+ * as they were; t0 + n may not exceed the longest request. */
+KVQ_API int kvq_read(kvq_handle *h, int layer, int t0, int n, void *K, void *V, void *stream);
 
 /* Free the handle (not the caller's workspace). */
 KVQ_API void kvq_destroy(kvq_handle *h);

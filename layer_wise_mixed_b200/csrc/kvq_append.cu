@@ -34,13 +34,22 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
 
+// Source slot of appended token i of `unit`'s request among its (b, h)'s token slots.
+__device__ __forceinline__ int src_slot(const AppendParams &p, int unit, int i) {
+    if (!p.index) return i;
+    const int s = p.index[static_cast<long long>(unit / p.Hkv) * p.n + i];
+    if (s >= 0 && s < p.n_src) return s;
+    atomicOr(p.status, kStatusBadIndex);
+    return 0;
+}
+
 // Per-token quantization of the new tokens of one 16-token half-block and repacking
 // of its words.  role 0 = keys (per-token mode), 1 = values.
 __device__ void per_token_half(const AppendParams &p, int role, int unit, int hbi, int L_old, int n,
                                uint8_t (*codes)[kMaxD], unsigned *cta_smax) {
     const int D = p.D, nj = D / 32;
     const int bits = role ? p.bv : p.bk;
-    const uint16_t *src = (role ? p.V : p.K) + static_cast<long long>(unit) * p.n * D;
+    const uint16_t *src = (role ? p.V : p.K) + static_cast<long long>(unit) * p.n_src * D;
     const int L_new = L_old + n;
     const int u0 = 16 * hbi;
     const int es = max(L_old, u0) - u0, ee = min(L_new, u0 + 16) - u0;
@@ -65,7 +74,7 @@ __device__ void per_token_half(const AppendParams &p, int role, int unit, int hb
     for (int it = warp; it < (ee - es) * nj; it += kWarps) {
         const int e = es + it / nj, j = it % nj;
         const int tok = u0 + e;
-        const uint16_t *row = src + static_cast<long long>(tok - L_old) * D;
+        const uint16_t *row = src + static_cast<long long>(src_slot(p, unit, tok - L_old)) * D;
         const int u = 16 * eta + e;
         {
             const float x = bf16_to_f32(row[32 * j + lane]);
@@ -115,14 +124,14 @@ __device__ void per_token_half(const AppendParams &p, int role, int unit, int hb
 __device__ void per_channel_group(const AppendParams &p, int unit, int q, bool do_group, bool first, int L_old,
                                   int n, float (*xs)[kMaxD], uint8_t (*codes)[kMaxD], unsigned *cta_smax) {
     const int D = p.D;
-    const uint16_t *src = p.K + static_cast<long long>(unit) * p.n * D;
+    const uint16_t *src = p.K + static_cast<long long>(unit) * p.n_src * D;
     uint16_t *res = p.res + static_cast<long long>(unit) * 32 * D;
     const int L_new = L_old + n;
     if (do_group) {
         const int t0 = 32 * q;
         for (int idx = threadIdx.x; idx < 32 * D; idx += kThreads) {
             const int u = idx / D, d = idx % D, tok = t0 + u;
-            const uint16_t v = tok < L_old ? res[u * D + d] : src[static_cast<long long>(tok - L_old) * D + d];
+            const uint16_t v = tok < L_old ? res[u * D + d] : src[static_cast<long long>(src_slot(p, unit, tok - L_old)) * D + d];
             xs[u][d] = bf16_to_f32(v);
         }
         __syncthreads();
@@ -164,7 +173,8 @@ __device__ void per_channel_group(const AppendParams &p, int unit, int q, bool d
         const int cnt = L_new - res_start;
         for (int idx = threadIdx.x; idx < cnt * D; idx += kThreads) {
             const int tok = res_start + idx / D, d = idx % D;
-            res[(tok % 32) * D + d] = src[static_cast<long long>(tok - L_old) * D + d];
+            res[(tok % 32) * D + d] =
+                src[static_cast<long long>(src_slot(p, unit, tok - L_old)) * D + d];
         }
     }
 }

@@ -443,8 +443,10 @@ bool layer_ragged(const kvq_handle *h, int layer) {
 }
 
 // Append n[b] tokens to request b (n == nullptr: n_max to every request); K, V hold
-// n_max token slots per (b, kv head).
-int append_impl(kvq_handle *h, int layer, const void *K, const void *V, const int *n, int n_max, void *stream) {
+// n_max token slots per (b, kv head)
+// (or, with a device index, the n_src slots it picks from).
+int append_impl(kvq_handle *h, int layer, const void *K, const void *V, const int *n, int n_max, void *stream,
+                const int *index = nullptr, int n_src = 0) {
     int rc = check_layer(h, layer);
     if (rc) return rc;
     if ((rc = check_bound(h))) return rc;
@@ -480,6 +482,9 @@ int append_impl(kvq_handle *h, int layer, const void *K, const void *V, const in
     p.bv = g.bv;
     p.kmode = g.kmode;
     p.n = n_max;
+    p.index = index;
+    p.n_src = index ? n_src : n_max;
+    p.status = reinterpret_cast<unsigned *>(h->ws + h->status_off);
     p.cap_blk = h->cap_blk;
     p.rec_bytes = g.rec_bytes;
     p.kc = g.kc;
@@ -522,7 +527,7 @@ int append_impl(kvq_handle *h, int layer, const void *K, const void *V, const in
     if (nV + nK > 0x7FFFFFFFLL) return fail(KVQ_EUNSUPPORTED, "append too large for one launch");
     p.nV = static_cast<int>(nV);
     p.nK = static_cast<int>(nK);
-    if (p.nV + p.nK == 0) return ok();   // no token appended: nothing changes (the slot neither)
+    if (p.nV == 0) return ok();          // no token appended: nothing changes (the slot neither)
     std::vector<int> bidx, bval;         // block pools: new table entries
     {
         std::vector<int> L_new(B);
@@ -1367,7 +1372,10 @@ int kvq_device_status(kvq_handle *h, void *stream, unsigned *flags) {
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     if (e != cudaSuccess) return cuda_fail(e, "status read");
     if (flags) *flags = v;
-    if (v) return fail(KVQ_EDEVICE, "device status 0x%x (a bounded wait expired)", v);
+    if (v)
+        return fail(KVQ_EDEVICE, "device status 0x%x (%s%s%s)", v,
+                    (v & kvq::kStatusWaitExpired) ? "a bounded wait expired" : "", v == 3 ? "; " : "",
+                    (v & kvq::kStatusBadIndex) ? "a slot index outside its source" : "");
     return ok();
 }
 
@@ -1482,6 +1490,278 @@ int kvq_decode_attn_noalloc(kvq_handle *h, int layer, const void *q, void *out, 
         if (e != cudaSuccess) return cuda_fail(e, "merge launch");
         note_write(h, st, -1);
     }
+    return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------
+// Steps of several tokens, score shapes, and reading the cache back.
+namespace {
+
+// The requests' cached lengths and query-token counts (nq, or nqs[b]) for a launch on st;
+// large ragged batches go through the device table dev ([2][B]), written on st.
+int fill_seq_lens(kvq_handle *h, int layer, kvq::SeqLens &s, int nq, const int *nqs, int *dev, cudaStream_t st) {
+    const int B = h->desc.batch;
+    const auto &len = h->rlen[layer];
+    s.B = B;
+    s.L = len[0];
+    s.nq = nqs ? nqs[0] : nq;
+    bool same = !layer_ragged(h, layer);
+    for (int b = 0; nqs && b < B; ++b) same = same && nqs[b] == nqs[0];
+    s.ragged = same ? 0 : 1;
+    if (same) return KVQ_OK;
+    if (B <= kvq::kMaxRagged) {
+        for (int b = 0; b < B; ++b) {
+            s.lens[b] = len[b];
+            s.nqs[b] = nqs ? nqs[b] : nq;
+        }
+        return KVQ_OK;
+    }
+    std::vector<int> table(len.begin(), len.end());
+    for (int b = 0; b < B; ++b) table.push_back(nqs ? nqs[b] : nq);
+    cudaError_t e = kvq::launch_set_table(dev, table.data(), static_cast<int>(table.size()), st);
+    if (e != cudaSuccess) return cuda_fail(e, "length table launch");
+    for (size_t i = 0; i < table.size(); i += 1000) note_write(h, st, -1);
+    s.dev = dev;
+    return KVQ_OK;
+}
+
+int check_score_opts(const kvq_score_opts *o) {
+    if (!o) return KVQ_OK;
+    if (!(o->softcap >= 0.f) || std::isinf(o->softcap)) return fail(KVQ_EINVAL, "softcap must be 0 or positive and finite");
+    if (o->window < 0) return fail(KVQ_EINVAL, "window must be >= 0 (got %d)", o->window);
+    if (!std::isfinite(o->scale)) return fail(KVQ_EINVAL, "scale must be finite");
+    if (o->alibi && !aligned(o->alibi, 4)) return fail(KVQ_EALIGN, "alibi must be 4-byte aligned");
+    return KVQ_OK;
+}
+
+long long tree_table_bytes(const kvq_handle *h) { return align256(8LL * h->desc.batch); }
+
+// Launch parameters that kvq_tree_attn and kvq_decode_attn_scored share, and the split of
+// the sequence: nk drafted keys at most per request.
+void tree_params(kvq_handle *h, int layer, const kvq_score_opts *o, int T, int nk, int max_splits, kvq::TreeParams &p) {
+    const LayerGeom &g = h->geom[layer];
+    p.rec = h->ws + g.rec_off;
+    p.res = g.res_off >= 0 ? reinterpret_cast<const uint16_t *>(h->ws + g.res_off) : nullptr;
+    p.smax = smax_slot(h, layer, static_cast<int>(h->ver[layer]));
+    p.btab = block_table(h, layer);
+    p.status = reinterpret_cast<unsigned *>(h->ws + h->status_off);
+    p.B = h->desc.batch;
+    p.Hkv = h->desc.n_kv_heads;
+    p.G = h->desc.n_q_heads / h->desc.n_kv_heads;
+    p.T = T;
+    p.cap_blk = h->cap_blk;
+    p.mask_words = (T + 31) / 32;
+    p.cap = o ? o->softcap : 0.f;
+    p.alibi = o ? o->alibi : nullptr;
+    p.window = o ? o->window : 0;
+    p.scale = o && o->scale != 0.f ? o->scale : 1.f / std::sqrt(static_cast<float>(h->desc.head_dim));
+    (void)nk;
+    (void)max_splits;
+    p.S = 1;
+}
+
+int tree_launch(kvq_handle *h, int layer, kvq::TreeParams &p, cudaStream_t st) {
+    const LayerGeom &g = h->geom[layer];
+    int rc = prepare_status(h, st);
+    if (rc) return rc;
+    cudaError_t e = kvq::launch_tree(p, h->desc.head_dim, g.bk, g.bv, g.kmode, st);
+    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    note_write(h, st, -1);
+    if (p.S > 1) {
+        e = kvq::launch_tree_merge(p, h->desc.head_dim, st);
+        if (e != cudaSuccess) return cuda_fail(e, "tree merge launch");
+        note_write(h, st, -1);
+    }
+    return ok();
+}
+
+constexpr int kMaxDraft = 4096;
+
+}  // namespace
+
+extern "C" {
+
+int kvq_norm_rope(kvq_handle *h, int layer, const void *qkv, int64_t batch_stride, int64_t token_stride, int n,
+                  const int32_t *offset, const kvq_rope_desc *rope, void *q, void *K, void *V, void *stream) {
+    int rc = check_layer(h, layer);
+    if (rc) return rc;
+    if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_norm_rope");
+    if ((rc = check_bound(h))) return rc;
+    if (!qkv || !rope || !q || !K || !V) return fail(KVQ_EINVAL, "null qkv, rope, q, K or V");
+    if (!aligned(qkv, 16) || !aligned(q, 16) || !aligned(K, 16) || !aligned(V, 16))
+        return fail(KVQ_EALIGN, "qkv, q, K and V must be 16-byte aligned");
+    if (n < 1) return fail(KVQ_EINVAL, "n must be >= 1 (got %d)", n);
+    const int D = h->desc.head_dim, Hq = h->desc.n_q_heads, Hkv = h->desc.n_kv_heads;
+    if (token_stride % 8 || batch_stride % 8 || batch_stride < 0 || token_stride < static_cast<int64_t>(Hq + 2 * Hkv) * D)
+        return fail(KVQ_EINVAL, "strides must be multiples of 8, token_stride at least (Hq + 2 Hkv) D = %d",
+                    (Hq + 2 * Hkv) * D);
+    if (rope->rot_dim < 0 || rope->rot_dim > D) return fail(KVQ_EINVAL, "rot_dim %d outside [0, %d]", rope->rot_dim, D);
+    if (rope->rot_dim % 16) return fail(KVQ_EUNSUPPORTED, "rot_dim must be a multiple of 16 (got %d)", rope->rot_dim);
+    if (rope->rot_dim > 0 && !rope->inv_freq) return fail(KVQ_EINVAL, "null inv_freq");
+    if (!aligned(rope->inv_freq, 4) || !aligned(rope->q_weight, 4) || !aligned(rope->k_weight, 4) || !aligned(offset, 4))
+        return fail(KVQ_EALIGN, "inv_freq, weights and offset must be 4-byte aligned");
+    if (!(rope->eps >= 0.f)) return fail(KVQ_EINVAL, "eps must be >= 0");
+    const long long tokens = static_cast<long long>(h->desc.batch) * n;
+    if (tokens > 0x7FFFFFFFLL) return fail(KVQ_EUNSUPPORTED, "too many tokens for one launch");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kvq::RopeParams p{};
+    p.qkv = static_cast<const uint16_t *>(qkv);
+    p.batch_stride = batch_stride;
+    p.token_stride = token_stride;
+    p.offset = offset;
+    p.inv_freq = rope->inv_freq;
+    p.wq = rope->q_weight;
+    p.wk = rope->k_weight;
+    p.q = static_cast<uint16_t *>(q);
+    p.K = static_cast<uint16_t *>(K);
+    p.V = static_cast<uint16_t *>(V);
+    p.B = h->desc.batch;
+    p.n = n;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.rot = rope->rot_dim;
+    p.interleaved = rope->interleaved ? 1 : 0;
+    p.eps = rope->eps;
+    if ((rc = fill_seq_lens(h, layer, p.len, n, nullptr, lens_table(h, layer), st))) return rc;
+    cudaError_t e = kvq::launch_rope(p, st);
+    if (e != cudaSuccess) return cuda_fail(e, "norm + rotation launch");
+    note_write(h, st, -1);
+    return ok();
+}
+
+int kvq_tree_attn_workspace_bytes(const kvq_handle *h, int T, size_t *bytes) {
+    if (!h || !bytes) return fail(KVQ_EINVAL, "null argument");
+    if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_tree_attn");
+    if (T < 1) return fail(KVQ_EINVAL, "T must be >= 1 (got %d)", T);
+    if (T > kMaxDraft) return fail(KVQ_EUNSUPPORTED, "T must be at most %d (got %d)", kMaxDraft, T);
+    const int G = h->desc.n_q_heads / h->desc.n_kv_heads;
+    const long long rows = static_cast<long long>(h->desc.batch) * T * h->desc.n_q_heads;
+    const int S = kvq::tree_max_splits(h->desc.batch, h->desc.n_kv_heads, T * G);
+    long long n = tree_table_bytes(h);
+    if (S > 1) n += align256(rows * S * h->desc.head_dim * 4) + align256(rows * S * 8);
+    *bytes = static_cast<size_t>(n);
+    return ok();
+}
+
+int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const void *V, int T, const int32_t *n_draft,
+                  const uint32_t *mask, const int32_t *depth, const kvq_score_opts *opts, void *out, int out_fp32,
+                  void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_layer(h, layer);
+    if (rc) return rc;
+    if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_tree_attn");
+    if ((rc = check_bound(h))) return rc;
+    if (!q || !K || !V || !out) return fail(KVQ_EINVAL, "null q, K, V or out");
+    if (!aligned(q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(out, 16))
+        return fail(KVQ_EALIGN, "q, K, V and out must be 16-byte aligned");
+    if (!aligned(mask, 4) || !aligned(depth, 4)) return fail(KVQ_EALIGN, "mask and depth must be 4-byte aligned");
+    size_t need = 0;
+    if ((rc = kvq_tree_attn_workspace_bytes(h, T, &need))) return rc;
+    if ((rc = check_score_opts(opts))) return rc;
+    const int B = h->desc.batch;
+    int nq_max = T;
+    if (n_draft) {
+        nq_max = 0;
+        for (int b = 0; b < B; ++b) {
+            if (n_draft[b] < 0 || n_draft[b] > T)
+                return fail(KVQ_EINVAL, "request %d: n_draft %d outside [0, %d]", b, n_draft[b], T);
+            nq_max = std::max(nq_max, static_cast<int>(n_draft[b]));
+        }
+    }
+    if (!workspace || workspace_bytes < need)
+        return fail(KVQ_EUNBOUND, "workspace too small: %zu < %zu bytes", workspace ? workspace_bytes : 0, need);
+    if (!aligned(workspace, 256)) return fail(KVQ_EALIGN, "workspace must be 256-byte aligned");
+    if (nq_max == 0) return ok();
+    const int G = h->desc.n_q_heads / h->desc.n_kv_heads;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kvq::TreeParams p{};
+    const int S = kvq::tree_max_splits(B, h->desc.n_kv_heads, T * G);
+    tree_params(h, layer, opts, T, nq_max, S, p);
+    p.q = static_cast<const uint16_t *>(q);
+    p.kd = static_cast<const uint16_t *>(K);
+    p.vd = static_cast<const uint16_t *>(V);
+    p.mask = mask;
+    p.depth = depth;
+    p.out = out;
+    p.out_fp32 = out_fp32 ? 1 : 0;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const long long rows = static_cast<long long>(B) * T * h->desc.n_q_heads;
+    p.part_acc = reinterpret_cast<float *>(ws + tree_table_bytes(h));
+    p.part_ml = reinterpret_cast<float *>(ws + tree_table_bytes(h) + align256(rows * S * h->desc.head_dim * 4));
+    p.sstride = S;
+    if ((rc = fill_seq_lens(h, layer, p.len, T, n_draft, reinterpret_cast<int *>(ws), st))) return rc;
+    return tree_launch(h, layer, p, st);
+}
+
+int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_score_opts *opts, void *out, int out_fp32,
+                           void *stream) {
+    int rc = check_layer(h, layer);
+    if (rc) return rc;
+    if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_decode_attn_scored");
+    if ((rc = check_bound(h))) return rc;
+    if (!q || !out) return fail(KVQ_EINVAL, "null q or out");
+    if (!aligned(q, 16) || !aligned(out, 16)) return fail(KVQ_EALIGN, "q and out must be 16-byte aligned");
+    if ((rc = check_score_opts(opts))) return rc;
+    for (int b = 0; b < h->desc.batch; ++b)
+        if (h->rlen[layer][b] < 1) return fail(KVQ_EINVAL, "layer %d: request %d is empty", layer, b);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kvq::TreeParams p{};
+    const int G = h->desc.n_q_heads / h->desc.n_kv_heads;
+    tree_params(h, layer, opts, 1, 0, std::min(kvq::kMaxSplits, kvq::tree_max_splits(h->desc.batch, h->desc.n_kv_heads, G)),
+                p);
+    p.q = static_cast<const uint16_t *>(q);
+    p.out = out;
+    p.out_fp32 = out_fp32 ? 1 : 0;
+    p.pos0 = -1;
+    p.part_acc = reinterpret_cast<float *>(h->ws + h->part_acc_off);
+    p.part_ml = reinterpret_cast<float *>(h->ws + h->part_ml_off);
+    p.sstride = kvq::kMaxSplits;
+    if ((rc = fill_seq_lens(h, layer, p.len, 1, nullptr, lens_table(h, layer), st))) return rc;
+    return tree_launch(h, layer, p, st);
+}
+
+int kvq_append_selected(kvq_handle *h, int layer, const void *K, const void *V, int n_src, const int32_t *index,
+                        const int32_t *n_new, int n_max, void *stream) {
+    int rc = check_layer(h, layer);
+    if (rc) return rc;
+    if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_append_selected");
+    if (!index) return fail(KVQ_EINVAL, "null index");
+    if (!aligned(index, 4)) return fail(KVQ_EALIGN, "index must be 4-byte aligned");
+    if (n_src < 1) return fail(KVQ_EINVAL, "n_src must be >= 1 (got %d)", n_src);
+    return append_impl(h, layer, K, V, n_new, n_max, stream, index, n_src);
+}
+
+int kvq_read(kvq_handle *h, int layer, int t0, int n, void *K, void *V, void *stream) {
+    int rc = check_layer(h, layer);
+    if (rc) return rc;
+    if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_read");
+    if ((rc = check_bound(h))) return rc;
+    if (!K && !V) return fail(KVQ_EINVAL, "null K and V");
+    if (!aligned(K, 16) || !aligned(V, 16)) return fail(KVQ_EALIGN, "K and V must be 16-byte aligned");
+    if (t0 < 0 || n < 1 || static_cast<long long>(t0) + n > h->len[layer])
+        return fail(KVQ_EINVAL, "tokens [%d, %lld) outside [0, %d)", t0, static_cast<long long>(t0) + n, h->len[layer]);
+    const LayerGeom &g = h->geom[layer];
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    kvq::ReadParams p{};
+    p.rec = h->ws + g.rec_off;
+    p.res = g.res_off >= 0 ? reinterpret_cast<const uint16_t *>(h->ws + g.res_off) : nullptr;
+    p.btab = block_table(h, layer);
+    p.K = static_cast<uint16_t *>(K);
+    p.V = static_cast<uint16_t *>(V);
+    p.B = h->desc.batch;
+    p.Hkv = h->desc.n_kv_heads;
+    p.cap_blk = h->cap_blk;
+    p.t0 = t0;
+    p.n = n;
+    p.blk0 = t0 / 32;
+    p.nblk = (t0 + n - 1) / 32 - p.blk0 + 1;
+    if (static_cast<long long>(p.B) * p.Hkv * p.nblk > 0x7FFFFFFFLL) return fail(KVQ_EUNSUPPORTED, "read too large for one launch");
+    if ((rc = fill_seq_lens(h, layer, p.len, 0, nullptr, lens_table(h, layer), st))) return rc;
+    cudaError_t e = kvq::launch_read(p, h->desc.head_dim, g.bk, g.bv, g.kmode, st);
+    if (e != cudaSuccess) return cuda_fail(e, "read launch");
+    note_write(h, st, -1);
     return ok();
 }
 

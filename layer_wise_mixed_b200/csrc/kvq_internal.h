@@ -59,6 +59,7 @@ constexpr int kDecodeWarps = 4;     // warps per decode CTA
 
 // Device status word bits (written with atomicOr, read by kvq_device_status).
 constexpr unsigned kStatusWaitExpired = 1u;   // a bounded mbarrier wait gave up
+constexpr unsigned kStatusBadIndex = 2u;      // kvq_append_selected met an index outside its source
 // Wall-time limit of one bounded wait inside a kernel (nanoseconds of the GPU's global
 // timer): 100 ms, far above any copy's latency, far below what would hold a GPU.
 constexpr unsigned long long kWaitLimitNs = 100ull * 1000 * 1000;
@@ -95,6 +96,12 @@ struct AppendParams {
     int L_old_r[kMaxRagged], n_r[kMaxRagged];
     const int *ragged_dev;
     const int *btab;            // block pools: [B][cap_blk] pool block of each block (rec is the pool)
+    // kvq_append_selected (index != null): K, V hold n_src token slots per (b, h) and appended
+    // token i of request b is slot index[b * n + i]; a slot outside [0, n_src) sets
+    // kStatusBadIndex in *status and slot 0 is taken.  Otherwise token i is slot i of n.
+    const int *index;
+    int n_src;
+    unsigned *status;
 };
 
 struct DecodeParams {
@@ -202,6 +209,69 @@ struct MergeParams {
 // round trip at its exit), nine (the paged 32K-context workload) with the in-launch merge.
 constexpr int kInLaunchMergeSplits = 4;
 
+// ---------------------------------------------------------------- queries of several tokens
+// Lengths of the requests of one launch: uniform, in the parameters (up to kMaxRagged
+// requests), or in a device table (larger ragged batches).
+struct SeqLens {
+    int ragged;                 // 0: every request has L cached tokens and nq query tokens
+    int L, nq;
+    int lens[kMaxRagged], nqs[kMaxRagged];
+    const int *dev;             // [B] lengths, then [B] query-token counts, or null
+    int B;
+#ifdef __CUDACC__
+    __device__ __forceinline__ int len(int b) const { return !ragged ? L : (dev ? dev[b] : lens[b]); }
+    __device__ __forceinline__ int queries(int b) const { return !ragged ? nq : (dev ? dev[B + b] : nqs[b]); }
+#endif
+};
+
+// Attention of T query tokens per request over the packed cache and (kd != null) over the
+// T drafted tokens themselves (kvq_tree_attn, kvq_decode_attn_scored).
+struct TreeParams {
+    const uint8_t *rec;         // layer records
+    const uint16_t *res;        // residual (per-channel keys) or null
+    const uint16_t *q;          // bf16 [B][T][Hq][D]
+    const uint16_t *kd, *vd;    // bf16 [B][Hkv][T][D], or null: cached tokens only
+    const uint32_t *mask;       // [B][T][mask_words], or null: token t sees tokens 0 .. t
+    const int *depth;           // [B][T] position of token t behind the cached ones, or null: t
+    const float *alibi;         // [Hq] slopes, or null
+    const unsigned *smax;       // this layer's {max key scale, max value scale} (fp16 bits)
+    const int *btab;
+    void *out;                  // [B][T][Hq][D] bf16 or fp32
+    float *part_acc;            // split partials: row r = (b T + t) Hq + hq, slot s: [r][sstride][D]
+    float *part_ml;             // [r][sstride][2]  (m in log2 units, l)
+    int sstride;
+    unsigned *status;
+    int B, Hkv, G, T, cap_blk, mask_words;
+    int S, tps;                 // splits, 128-token tiles per split
+    int pos0;                   // query position - cached length - depth (0; -1: the last cached token)
+    int window;                 // 0: none
+    float cap, scale;           // cap 0: none; scale of q . k
+    int out_fp32;
+    SeqLens len;
+};
+
+// Tokens [t0, t0 + n) of a layer as bf16 (kvq_read).
+struct ReadParams {
+    const uint8_t *rec;
+    const uint16_t *res;
+    const int *btab;
+    uint16_t *K, *V;            // bf16 [B][Hkv][n][D], either may be null
+    int B, Hkv, cap_blk, t0, n, blk0, nblk;
+    SeqLens len;
+};
+
+// kvq_norm_rope
+struct RopeParams {
+    const uint16_t *qkv;        // bf16, token (b, i) at b * batch_stride + i * token_stride
+    long long batch_stride, token_stride;
+    const int *offset;          // [B][n] or null: i
+    const float *inv_freq, *wq, *wk;
+    uint16_t *q, *K, *V;        // [B][n][Hq][D], [B][Hkv][n][D] x 2
+    int B, n, Hq, Hkv, D, rot, interleaved;
+    float eps;
+    SeqLens len;
+};
+
 // Set the thread's kvq_last_error message and return code / clear it and return KVQ_OK
 // (for entry points outside kvq_host.cu).
 int host_fail(int code, const char *msg);
@@ -237,6 +307,14 @@ cudaError_t launch_paged_scan(const uint8_t *tags, int B, int n, int *inv2, int 
 cudaError_t launch_paged_append(const PagedAppendParams &p, int grid, cudaStream_t st);
 int paged_rec2_bytes(int D);
 int paged_page4_bytes(int D);
+cudaError_t launch_tree(const TreeParams &p, int D, int bk, int bv, int kmode, cudaStream_t st);
+cudaError_t launch_tree_merge(const TreeParams &p, int D, cudaStream_t st);
+// Row groups (CTAs of one split of one unit) of a launch with `rows` query rows per kv head,
+// and the most splits that launch_tree uses: what the partials are sized for.
+int tree_row_groups(int rows);
+int tree_max_splits(int B, int Hkv, int rows);
+cudaError_t launch_read(const ReadParams &p, int D, int bk, int bv, int kmode, cudaStream_t st);
+cudaError_t launch_rope(const RopeParams &p, cudaStream_t st);
 int decode_stages(long long rec_bytes, int D, int G);
 size_t decode_smem_bytes(long long rec_bytes, int nstage, int nextra, int D, int G);
 

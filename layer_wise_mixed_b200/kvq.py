@@ -53,6 +53,16 @@ class kvq_plan_desc(ctypes.Structure):
                 ("pool_blocks", ctypes.c_int)]
 
 
+class kvq_rope_desc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
+class kvq_score_opts(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("alibi", ctypes.c_void_p), ("window", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -88,6 +98,13 @@ def load() -> ctypes.CDLL:
         "kvq_tag_allocate": (I, [I, P, P, P, ctypes.c_double, P, P]),
         "kvq_tag_distortion_workspace_bytes": (I, [I, I, I, I, I, I, I, ctypes.POINTER(SZ)]),
         "kvq_tag_distortion_device": (I, [I, I, I, I, I, I, P, P, P, P, I, P, SZ, P, P, P, P]),
+        "kvq_norm_rope": (I, [P, I, P, ctypes.c_int64, ctypes.c_int64, I, P, ctypes.POINTER(kvq_rope_desc), P, P, P,
+                              P]),
+        "kvq_tree_attn_workspace_bytes": (I, [P, I, ctypes.POINTER(SZ)]),
+        "kvq_tree_attn": (I, [P, I, P, P, P, I, P, P, P, ctypes.POINTER(kvq_score_opts), P, I, P, SZ, P]),
+        "kvq_decode_attn_scored": (I, [P, I, P, ctypes.POINTER(kvq_score_opts), P, I, P]),
+        "kvq_append_selected": (I, [P, I, P, P, I, P, P, I, P]),
+        "kvq_read": (I, [P, I, I, I, P, P, P]),
         "kvq_destroy": (None, [P]),
         "kvq_last_error": (ctypes.c_char_p, []),
     }
@@ -303,6 +320,77 @@ def kvq_tag_allocate(D2, D4, counts, avg_bits: float):
     return bits, total.value
 
 
+def _opt_ptr(x):
+    return None if x is None else _ptr(x)
+
+
+def _host_i32(x):
+    """(pointer, array kept alive) of an optional host int32 array."""
+    if x is None:
+        return None, None
+    a = np.ascontiguousarray(x, np.int32)
+    return a.ctypes.data_as(ctypes.c_void_p), a
+
+
+def kvq_norm_rope(h: int, layer: int, qkv, batch_stride: int, token_stride: int, n: int, offset, rope: kvq_rope_desc,
+                  q, K, V, stream=None):
+    _check(load().kvq_norm_rope(h, layer, _ptr(qkv), batch_stride, token_stride, n, _opt_ptr(offset),
+                                ctypes.byref(rope), _ptr(q), _ptr(K), _ptr(V), _stream(stream)))
+
+
+def kvq_tree_attn_workspace_bytes(h: int, T: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().kvq_tree_attn_workspace_bytes(h, T, ctypes.byref(n)))
+    return n.value
+
+
+def kvq_tree_attn(h: int, layer: int, q, K, V, T: int, n_draft, mask, depth, opts: Optional[kvq_score_opts], out,
+                  out_fp32: bool, workspace, workspace_bytes: int, stream=None):
+    nd, keep = _host_i32(n_draft)
+    _check(load().kvq_tree_attn(h, layer, _ptr(q), _ptr(K), _ptr(V), T, nd, _opt_ptr(mask), _opt_ptr(depth),
+                                None if opts is None else ctypes.byref(opts), _ptr(out), int(bool(out_fp32)),
+                                _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def kvq_decode_attn_scored(h: int, layer: int, q, opts: Optional[kvq_score_opts], out, out_fp32: bool, stream=None):
+    _check(load().kvq_decode_attn_scored(h, layer, _ptr(q), None if opts is None else ctypes.byref(opts), _ptr(out),
+                                         int(bool(out_fp32)), _stream(stream)))
+
+
+def kvq_append_selected(h: int, layer: int, K, V, n_src: int, index, n_new, n_max: int, stream=None):
+    nn, keep = _host_i32(n_new)
+    _check(load().kvq_append_selected(h, layer, _ptr(K), _ptr(V), n_src, _ptr(index), nn, n_max, _stream(stream)))
+
+
+def kvq_read(h: int, layer: int, t0: int, n: int, K, V, stream=None):
+    _check(load().kvq_read(h, layer, t0, n, _opt_ptr(K), _opt_ptr(V), _stream(stream)))
+
+
+class Rope(kvq_rope_desc):
+    """kvq_rope_desc from tensors: inv_freq fp32 [rot_dim / 2], weights fp32 [head_dim] or None
+    (CUDA, kept alive here)."""
+
+    def __init__(self, rot_dim, inv_freq=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False):
+        for t in (inv_freq, q_weight, k_weight):
+            if t is not None and (str(t.dtype) != "torch.float32" or not t.is_contiguous()):
+                raise ValueError("inv_freq and weights must be contiguous float32")
+        if inv_freq is not None and inv_freq.numel() < rot_dim // 2:
+            raise ValueError("inv_freq has fewer than rot_dim / 2 entries")
+        super().__init__(rot_dim, int(bool(interleaved)), _opt_ptr(inv_freq), _opt_ptr(q_weight), _opt_ptr(k_weight),
+                         eps)
+        self.tensors = (inv_freq, q_weight, k_weight)
+
+
+class ScoreOpts(kvq_score_opts):
+    """kvq_score_opts; alibi: fp32 CUDA tensor [n_q_heads] or None (kept alive here)."""
+
+    def __init__(self, softcap=0.0, alibi=None, window=0, scale=0.0):
+        if alibi is not None and (str(alibi.dtype) != "torch.float32" or not alibi.is_contiguous()):
+            raise ValueError("alibi must be contiguous float32")
+        super().__init__(softcap, _opt_ptr(alibi), window, scale)
+        self.alibi_tensor = alibi
+
+
 # ------------------------------------------------------------------ convenience owner
 def make_paged_desc(num_layers: int, batch: int, n_kv_heads: int, n_q_heads: int, head_dim: int, max_ctx: int,
                     avg_bits: float):
@@ -374,6 +462,125 @@ class Cache:
 
     def seq_lens(self, layer):
         return kvq_seq_lens(self.h, layer, self.B)
+
+    # -------- steps of several tokens, score shapes, reading back
+    def _tensor(self, t, name, shape, dtype=None):
+        """Check one tensor argument: shape, type, device, contiguity."""
+        import torch
+        dtype = dtype or torch.bfloat16
+        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+            raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t.device != self.ws.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.ws.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+    def _out(self, t, name, shape, dtype=None):
+        import torch
+        if t is None:
+            return torch.empty(shape, dtype=dtype or torch.bfloat16, device=self.ws.device)
+        self._tensor(t, name, shape, dtype)
+        return t
+
+    def _head_weights(self, rope):
+        for t, name in ((rope.tensors[1], "q_weight"), (rope.tensors[2], "k_weight")):
+            if t is not None and t.numel() != self.D:
+                raise ValueError(f"{name} must have head_dim = {self.D} entries")
+
+    def _slopes(self, opts):
+        if opts is not None and opts.alibi_tensor is not None and opts.alibi_tensor.numel() != self.Hq:
+            raise ValueError(f"alibi must have one slope per query head ({self.Hq})")
+
+    def norm_rope(self, layer, qkv, rope, offset=None, q=None, K=None, V=None, stream=None):
+        """qkv bf16 [B, n, (Hq + 2 Hkv) * D] (rows may be padded); rope a Rope; offset int32
+        [B, n] positions behind the cached tokens, None: 0 .. n - 1.  Returns (q [B, n, Hq, D],
+        K, V [B, Hkv, n, D])."""
+        import torch
+        if qkv.dim() != 3 or qkv.shape[0] != self.B or qkv.shape[2] != (self.Hq + 2 * self.Hkv) * self.D:
+            raise ValueError(f"qkv: expected [{self.B}, n, {(self.Hq + 2 * self.Hkv) * self.D}], got {tuple(qkv.shape)}")
+        if qkv.dtype != torch.bfloat16 or qkv.stride(2) != 1 or qkv.device != self.ws.device:
+            raise ValueError("qkv must be bfloat16 on the cache's device with adjacent channels")
+        n = qkv.shape[1]
+        if offset is not None:
+            self._tensor(offset, "offset", (self.B, n), torch.int32)
+        self._head_weights(rope)
+        with torch.cuda.device(self.ws.device):
+            q = self._out(q, "q", (self.B, n, self.Hq, self.D))
+            K = self._out(K, "K", (self.B, self.Hkv, n, self.D))
+            V = self._out(V, "V", (self.B, self.Hkv, n, self.D))
+            # a dimension of size 1 may carry any stride: give the packed one
+            row = (self.Hq + 2 * self.Hkv) * self.D
+            ts = qkv.stride(1) if n > 1 else row
+            bs = qkv.stride(0) if self.B > 1 else 0
+            kvq_norm_rope(self.h, layer, qkv, bs, ts, n, offset, rope, q, K, V, stream)
+        return q, K, V
+
+    def tree_workspace(self, T):
+        """Workspace for tree_attn with T drafted tokens (uint8, 256-byte aligned)."""
+        import torch
+        return torch.empty(kvq_tree_attn_workspace_bytes(self.h, T), dtype=torch.uint8, device=self.ws.device)
+
+    def tree_attn(self, layer, q, K, V, n_draft=None, mask=None, depth=None, opts=None, out=None, out_fp32=False,
+                  workspace=None, stream=None):
+        """T drafted tokens over the cache and one another: q [B, T, Hq, D], K, V [B, Hkv, T, D];
+        n_draft host ints [B]; mask int32 [B, T, ceil(T / 32)] bits; depth int32 [B, T]; opts a
+        ScoreOpts.  workspace: one that tree_workspace(T) gave; calls that may overlap (other
+        streams, captured graphs) need one each.  Rows of a fresh `out` behind n_draft[b] are
+        unset."""
+        import torch
+        T = q.shape[1]
+        self._tensor(q, "q", (self.B, T, self.Hq, self.D))
+        self._tensor(K, "K", (self.B, self.Hkv, T, self.D))
+        self._tensor(V, "V", (self.B, self.Hkv, T, self.D))
+        if n_draft is not None and len(n_draft) != self.B:
+            raise ValueError(f"n_draft must have {self.B} entries")
+        if mask is not None:
+            self._tensor(mask, "mask", (self.B, T, (T + 31) // 32), torch.int32)
+        if depth is not None:
+            self._tensor(depth, "depth", (self.B, T), torch.int32)
+        self._slopes(opts)
+        with torch.cuda.device(self.ws.device):
+            out = self._out(out, "out", (self.B, T, self.Hq, self.D), torch.float32 if out_fp32 else torch.bfloat16)
+            ws = self.tree_workspace(T) if workspace is None else workspace
+            if workspace is None and stream is not None and not isinstance(stream, int):
+                ws.record_stream(stream)   # the call's own workspace outlives the launches on `stream`
+            kvq_tree_attn(self.h, layer, q, K, V, T, n_draft, mask, depth, opts, out, out_fp32, ws, ws.numel(), stream)
+        return out
+
+    def decode_attn_scored(self, layer, q, opts=None, out=None, out_fp32=False, stream=None):
+        """decode_attn with capped scores, distance bias or a sliding window (a ScoreOpts)."""
+        import torch
+        self._tensor(q, "q", (self.B, self.Hq, self.D))
+        self._slopes(opts)
+        with torch.cuda.device(self.ws.device):
+            out = self._out(out, "out", (self.B, self.Hq, self.D), torch.float32 if out_fp32 else torch.bfloat16)
+            kvq_decode_attn_scored(self.h, layer, q, opts, out, out_fp32, stream)
+        return out
+
+    def append_selected(self, layer, K, V, index, n_new=None, stream=None):
+        """Append slots index[b, :n_new[b]] (int32 [B, n_max]) of K, V [B, Hkv, n_src, D]."""
+        import torch
+        n_src = K.shape[2]
+        self._tensor(K, "K", (self.B, self.Hkv, n_src, self.D))
+        self._tensor(V, "V", (self.B, self.Hkv, n_src, self.D))
+        self._tensor(index, "index", (self.B, index.shape[-1]), torch.int32)
+        if n_new is not None and len(n_new) != self.B:
+            raise ValueError(f"n_new must have {self.B} entries")
+        with torch.cuda.device(self.ws.device):
+            kvq_append_selected(self.h, layer, K, V, n_src, index, n_new, index.shape[1], stream)
+
+    def read(self, layer, t0, n, K=None, V=None, stream=None):
+        """Tokens [t0, t0 + n) as bf16 (K, V [B, Hkv, n, D]); rows behind a shorter sequence's
+        last token are left as they were."""
+        import torch
+        with torch.cuda.device(self.ws.device):
+            K = self._out(K, "K", (self.B, self.Hkv, n, self.D))
+            V = self._out(V, "V", (self.B, self.Hkv, n, self.D))
+            kvq_read(self.h, layer, t0, n, K, V, stream)
+        return K, V
+
+    def truncate(self, layer, L):
+        kvq_truncate(self.h, layer, L)
 
     def export_layer(self, layer):
         return kvq_export_layer(self.h, layer)
