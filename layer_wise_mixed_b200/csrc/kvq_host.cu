@@ -1557,16 +1557,24 @@ void tree_params(kvq_handle *h, int layer, const kvq_score_opts *o, int T, int n
     p.alibi = o ? o->alibi : nullptr;
     p.window = o ? o->window : 0;
     p.scale = o && o->scale != 0.f ? o->scale : 1.f / std::sqrt(static_cast<float>(h->desc.head_dim));
-    (void)nk;
-    (void)max_splits;
-    p.S = 1;
+    p.bk = g.bk;
+    p.bv = g.bv;
+    p.kmode = g.kmode;
+    // tiles of the longest request: drafted keys and the open group, then whole blocks (those
+    // that the window of the earliest query leaves, positions taken as in a chunk)
+    const int L = h->len[layer];
+    const int open = g.kmode == KVQ_PER_CHANNEL ? L % 32 : 0;
+    const long long seen = p.window ? std::min<long long>(L, static_cast<long long>(p.window) + 128) : L;
+    const long long tiles = (open + nk + 127) / 128 + (seen - open + 127) / 128;
+    const int groups = kvq::tree_row_groups(T * p.G, g.bk, g.bv, h->desc.head_dim);
+    p.S = h->forced_splits > 0 ? static_cast<int>(std::min<long long>(std::min(h->forced_splits, max_splits), std::max(1LL, tiles)))
+                               : kvq::tree_splits(p.B, p.Hkv, groups, tiles, max_splits);
 }
 
-int tree_launch(kvq_handle *h, int layer, kvq::TreeParams &p, cudaStream_t st) {
-    const LayerGeom &g = h->geom[layer];
+int tree_launch(kvq_handle *h, kvq::TreeParams &p, cudaStream_t st) {
     int rc = prepare_status(h, st);
     if (rc) return rc;
-    cudaError_t e = kvq::launch_tree(p, h->desc.head_dim, g.bk, g.bv, g.kmode, st);
+    cudaError_t e = kvq::launch_tree(p, h->desc.head_dim, st);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
     note_write(h, st, -1);
     if (p.S > 1) {
@@ -1692,7 +1700,7 @@ int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const 
     p.part_ml = reinterpret_cast<float *>(ws + tree_table_bytes(h) + align256(rows * S * h->desc.head_dim * 4));
     p.sstride = S;
     if ((rc = fill_seq_lens(h, layer, p.len, T, n_draft, reinterpret_cast<int *>(ws), st))) return rc;
-    return tree_launch(h, layer, p, st);
+    return tree_launch(h, p, st);
 }
 
 int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_score_opts *opts, void *out, int out_fp32,
@@ -1719,7 +1727,7 @@ int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_sc
     p.part_ml = reinterpret_cast<float *>(h->ws + h->part_ml_off);
     p.sstride = kvq::kMaxSplits;
     if ((rc = fill_seq_lens(h, layer, p.len, 1, nullptr, lens_table(h, layer), st))) return rc;
-    return tree_launch(h, layer, p, st);
+    return tree_launch(h, p, st);
 }
 
 int kvq_append_selected(kvq_handle *h, int layer, const void *K, const void *V, int n_src, const int32_t *index,

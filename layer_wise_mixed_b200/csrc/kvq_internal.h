@@ -242,11 +242,13 @@ struct TreeParams {
     int sstride;
     unsigned *status;
     int B, Hkv, G, T, cap_blk, mask_words;
-    int S, tps;                 // splits, 128-token tiles per split
+    int S;                      // splits of every request's tiles (even parts)
     int pos0;                   // query position - cached length - depth (0; -1: the last cached token)
     int window;                 // 0: none
     float cap, scale;           // cap 0: none; scale of q . k
     int out_fp32;
+    int bk, bv, kmode;
+    int dk, dv;                 // packed-block stages of each key / value warp (set by launch_tree)
     SeqLens len;
 };
 
@@ -307,12 +309,14 @@ cudaError_t launch_paged_scan(const uint8_t *tags, int B, int n, int *inv2, int 
 cudaError_t launch_paged_append(const PagedAppendParams &p, int grid, cudaStream_t st);
 int paged_rec2_bytes(int D);
 int paged_page4_bytes(int D);
-cudaError_t launch_tree(const TreeParams &p, int D, int bk, int bv, int kmode, cudaStream_t st);
+cudaError_t launch_tree(const TreeParams &p, int D, cudaStream_t st);
 cudaError_t launch_tree_merge(const TreeParams &p, int D, cudaStream_t st);
 // Row groups (CTAs of one split of one unit) of a launch with `rows` query rows per kv head,
-// and the most splits that launch_tree uses: what the partials are sized for.
-int tree_row_groups(int rows);
+// the most splits a launch may use (what partials are sized for), and the split count for
+// `tiles` 128-token tiles per unit.
+int tree_row_groups(int rows, int bk, int bv, int D);
 int tree_max_splits(int B, int Hkv, int rows);
+int tree_splits(int B, int Hkv, int row_groups, long long tiles, int max_splits);
 cudaError_t launch_read(const ReadParams &p, int D, int bk, int bv, int kmode, cudaStream_t st);
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t st);
 int decode_stages(long long rec_bytes, int D, int G);

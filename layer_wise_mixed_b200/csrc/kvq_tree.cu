@@ -1,7 +1,44 @@
 // Attention of several query tokens per request over the packed cache and over the drafted
-// tokens themselves (sm_100a): the plain form, one warp per query row.
+// tokens themselves (kvq_tree_attn), and of one query token with score shapes
+// (kvq_decode_attn_scored), on the 5th-generation tensor cores (sm_100a).
+//
+//   s = scale q.k^,  s = cap tanh(s / cap),  s -= slope (pos_q - pos_k);  out = softmax(s) v^
+//
+// The T * G query rows that share a kv head form row tiles of 128.  A CTA (one per SM) runs a
+// part of one unit's keys against one row tile, or two (TWO): each packed block is then
+// unpacked once for up to 256 rows.  Roles:
+//   warps 0-7   softmax: two slots of 128 threads, a thread per query row.  TWO: slot j has
+//               row tile j; otherwise both slots have the one row tile and take the key tiles
+//               in turn (even, odd), each with its own sums, joined at the end.
+//   warps 8-15  unpack: warp 8 + w writes key block w (of 4) of each 128-token tile as fp16
+//               code * scale + zero, warp 12 + w the value block; packed parts come through
+//               the warp's own ring of cp.async stages.
+//   warp 16     one thread issues the MMAs: S = Q K^T (operands in shared memory), O += P V
+//               (P in tensor memory over S's first columns).
+// While one slot is in its softmax the other's MMAs run.
+//
+// Tiles.  First the "open" ones, keys that are bf16: the open per-channel key group (bf16
+// residual, values from its packed block), then the drafted tokens.  Then the whole packed
+// blocks, four to a tile.  Every operand is fp16 in the 128-byte-swizzled K-major layout.
+// The channel order inside a key or query row and the token order inside a tile are permuted
+// (both operands of a product alike) so that a lane's unpacked pairs are one 16-byte store
+// without bank conflicts:
+//   channel d = 64 ks + 32 i + 16 k + 8 r + 2 t + hb  ->  64 ks + 16 t + 8 i + 4 k + 2 r + hb
+//   token u of block w: u = 16 kk + 8 ch + 2 t + hb   ->  64 (w / 2) + 16 t + 8 (w % 2) + 4 kk + 2 ch + hb
+// (the open tiles keep their tokens in order).
+//
+// Roundings.  A cached key or value is one fp16 FMA of its exact code: off by 2^-11 of itself
+// at most, and exact where the scale and zero are subnormal.  Query rows and bf16 key rows are
+// scaled by a power of two to below 2^15 (exact in fp16 to 2^-38 of the row's largest);
+// layers whose largest scale would leave fp16's range are scaled down as a whole.  Weights
+// are fp16 of 2^(s - m + 7): m follows the running maximum, and lags by up to 2^8 so that
+// the sums in tensor memory are rescaled only when it grew by more.  Scores, m, l and O are
+// fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
@@ -11,118 +48,977 @@ namespace kvq {
 namespace {
 
 constexpr float kLog2eT = 1.4426950408889634f;
+constexpr int kTreeThreads = 17 * 32;
+constexpr int kTile = 128;              // tokens of a key tile, rows of a row tile
+constexpr float kWeightBias = 7.f;      // weights are 2^(s - m + 7), s - m <= 8
+constexpr float kLag = 8.f;
+constexpr uint32_t kTmemCols = 512;     // S0, S1, O0, O1
 
-__device__ __forceinline__ float field_value(const uint8_t *codes, const uint8_t *sz, int role, bool per_token, int u,
-                                             int d, int D, int bits) {
-    int word, bit;
-    quant::code_place(role, u & 15, d, D, bits, word, bit);
-    const uint32_t w = reinterpret_cast<const uint32_t *>(codes + (u >> 4) * 2 * D * bits)[word];
-    const int nj = D / 32;
-    const int so = per_token ? quant::tok_sz_off(u, d / 32, nj) : quant::chan_sz_off(d);
-    const int zo = so + (per_token ? 4 * nj : 4);
-    return fmaf(static_cast<float>((w >> bit) & ((1u << bits) - 1u)),
-                __half2float(*reinterpret_cast<const __half *>(sz + so)),
-                __half2float(*reinterpret_cast<const __half *>(sz + zo)));
+// ------------------------------------------------------------------ tcgen05
+// Shared-memory descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor of kind::f16: fp16 operands (K-major), fp32 accumulator, M x N.
+__host__ __device__ constexpr uint32_t f16_idesc(int M, int N) {
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__global__ void __launch_bounds__(128) tree_row_kernel(const TreeParams p, int D, int bk, int bv, int kmode) {
-    pdl_enter();
-    __shared__ float qs[4][128], ps[4][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int Hq = p.Hkv * p.G;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;   // (b T + t) Hq + hq
-    if (row >= static_cast<long long>(p.B) * p.T * Hq) return;
-    const int hq = static_cast<int>(row % Hq), t = static_cast<int>(row / Hq % p.T), b = static_cast<int>(row / Hq / p.T);
-    const int nq = p.len.queries(b), L = p.len.len(b), h = hq / p.G;
-    if (t >= nq) return;
-    const long long unit = static_cast<long long>(b) * p.Hkv + h;
-    const int rec_bytes = 4 * D * bk + 4 * D + 4 * D * bv + 4 * D;
-    const int depth = p.depth ? p.depth[b * p.T + t] : t;
-    const int pos = L + p.pos0 + (p.kd ? depth : 0);
-    const float slope = p.alibi ? p.alibi[hq] : 0.f;
-    for (int d = lane; d < D; d += 32) qs[warp][d] = quant::bf16_to_f32(p.q[row * D + d]);
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const int nk = p.kd ? nq : 0;
-    for (int t0 = 0; t0 < L + nk;) {
-        const bool cached = t0 < L;
-        const int n = cached ? min(32, L - t0) : min(32, L + nk - t0);
-        const int blk = t0 >> 5, j0 = t0 - L;
-        const uint8_t *rec = cached ? p.rec + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk) * rec_bytes : nullptr;
-        const bool open = cached && kmode == 0 && blk == (L >> 5);
-        float s = -INFINITY;
-        if (lane < n) {
-            bool see = true;
-            int kpos = t0 + lane;
-            const uint16_t *krow = nullptr;
-            if (!cached) {
-                const int j = j0 + lane;
-                see = p.mask ? (p.mask[(static_cast<long long>(b) * p.T + t) * p.mask_words + (j >> 5)] >> (j & 31)) & 1
-                             : j <= t;
-                kpos = L + (p.depth ? p.depth[b * p.T + j] : j);
-                krow = p.kd + (unit * p.T + j) * D;
-            } else if (open) krow = p.res + (unit * 32 + lane) * D;
-            if (p.window && pos - kpos >= p.window) see = false;
-            if (see) {
-                float a = 0.f;
-                for (int d = 0; d < D; ++d)
-                    a = fmaf(qs[warp][d],
-                             krow ? quant::bf16_to_f32(krow[d])
-                                  : field_value(rec, rec + 4 * D * bk, 0, kmode == 1, lane, d, D, bk), a);
-                a *= p.scale;
-                if (p.cap > 0.f) a = p.cap * tanhf(a / p.cap);
-                s = a - slope * static_cast<float>(pos - kpos);
-            }
-        }
-        float mx = s;
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mn = fmaxf(m, mx);
-        if (mn > -INFINITY || __any_sync(0xffffffffu, s != s)) {
-            const float al = exp2f((m - mn) * kLog2eT);
-            const float e = s == -INFINITY ? 0.f : exp2f((s - mn) * kLog2eT);
-            ps[warp][lane] = e;
-            float sum = e;
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float a0 = m == -INFINITY ? 0.f : al;
-            l = l * a0 + sum;
-            m = mn;
-            __syncwarp();
-            for (int c = 0; c < D / 32; ++c) {
-                const int d = 32 * c + lane;
-                float a = acc[c] * a0;
-                for (int u = 0; u < n; ++u) {
-                    const float w = ps[warp][u];
-                    if (w == 0.f) continue;
-                    const float v = cached ? field_value(rec + 4 * D * bk + 4 * D, rec + 4 * D * bk + 4 * D + 4 * D * bv, 1,
-                                                         true, u, d, D, bv)
-                                           : quant::bf16_to_f32(p.vd[(unit * p.T + j0 + u) * D + d]);
-                    a = fmaf(w, v, a);
+#define KVQ_R8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+// 32 columns of this warp's 32 lanes, one per register; the registers hold the values after
+// ld32_wait on the same array.
+__device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void ld32_wait(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : KVQ_R8(r, 0), KVQ_R8(r, 8), KVQ_R8(r, 16), KVQ_R8(r, 24)::"memory");
+}
+__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------------ shared memory
+// Offsets of one CTA's dynamic shared memory (1024-byte aligned base).
+template <int D, bool TWO>
+struct TreeSmem {
+    static constexpr int OPER = kTile * D * 2;                  // one operand tile
+    static constexpr int q = 0;                                 // query row tiles
+    static constexpr int k = q + (TWO ? 2 : 1) * OPER;          // two key tiles
+    static constexpr int v = k + 2 * OPER;                      // two value tiles [D channels][128 tokens]
+    static constexpr int rowscale = v + 2 * OPER;               // score scale of each query row [256]
+    // open tiles: key row scales and positions, [4][128] each (tile i uses stage i % 4: when its
+    // keys are written, tile i - 2's scores are done, so tile i - 4's softmax is)
+    static constexpr int kscale = rowscale + 256 * 4;
+    static constexpr int kpos = kscale + 4 * kTile * 4;
+    static constexpr int ml = kpos + 4 * kTile * 4;             // [2][128] (m, l) to join the slots
+    static constexpr int bars = ml + (TWO ? 0 : 2 * kTile * 8); // barriers, TMEM address, flags
+    static constexpr int ring = bars + 256;                     // packed parts
+};
+// Joining two slots (one row tile): each hands half its channels over, rows of D / 2 + 4 floats
+// in the operand tiles (free by then).
+template <int D>
+constexpr int kJoinRow = D / 2 + 4;
+static_assert(2 * kTile * kJoinRow<128> * 4 <= TreeSmem<128, false>::v, "the join area is the query and key tiles");
+static_assert(2 * kTile * kJoinRow<64> * 4 <= TreeSmem<64, false>::v, "the join area is the query and key tiles");
+
+struct TreeBars {
+    uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2];
+    uint32_t tmem, bad_value;
+    int min_pos;
+};
+static_assert(sizeof(TreeBars) <= 256, "barrier area");
+
+// Position of token `col` of a packed tile within the tile's 128 tokens.
+__host__ __device__ constexpr int tile_token(int col) {
+    return 32 * (2 * (col >> 6) + ((col >> 3) & 1)) + 16 * ((col >> 2) & 1) + 8 * ((col >> 1) & 1) + 2 * ((col >> 4) & 3) +
+           (col & 1);
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait(int pending) {   // at most `pending` groups still in flight
+    if (pending == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t hfma2_bits(uint32_t c, uint32_t s, uint32_t z) {
+    return h2_bits(__hfma2(bits_h2(c), bits_h2(s), bits_h2(z)));
+}
+__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) { return h2_bits(__hmul2(bits_h2(a), bits_h2(b))); }
+
+// Key block w of a tile (part: [codes][s/z] in shared memory) -> fp16 rows of the K operand.
+// pre: an exact power of two (half2) when the layer's values would leave fp16's range, else 0.
+template <int BK, int KM, int D>
+__device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, int w, int lane, uint32_t pre) {
+    constexpr int NJ = D / 32, PK = 16 / BK, WHK = D * BK / 64, KC = 4 * D * BK;
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t kw[2][WHK];
+    load_lane_words<WHK>(part, lane, kw[0]);
+    load_lane_words<WHK>(part + 2 * D * BK, lane, kw[1]);
+    // row of token u = 16 kk + 8 i + g, n = 2 kk + i: row0 + 4 kk + 2 i
+    const int row0 = 64 * (w >> 1) + 16 * (g >> 1) + 8 * (w & 1) + (g & 1);
+#pragma unroll
+    for (int ks = 0; ks < D / 64; ++ks)
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2) {
+            uint32_t s[2][2], z[2][2];   // [k][r] (per-channel keys)
+            if constexpr (KM == 0) {
+#pragma unroll
+                for (int k1 = 0; k1 < 2; ++k1) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(part + KC + 16 * (4 * (4 * ks + 2 * i2 + k1) + t));
+                    s[k1][0] = a.x; z[k1][0] = a.y; s[k1][1] = a.z; z[k1][1] = a.w;
+                    if (pre) {
+                        s[k1][0] = hmul2_bits(s[k1][0], pre); z[k1][0] = hmul2_bits(z[k1][0], pre);
+                        s[k1][1] = hmul2_bits(s[k1][1], pre); z[k1][1] = hmul2_bits(z[k1][1], pre);
+                    }
                 }
-                acc[c] = a;
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                uint32_t st = 0, zt = 0;
+                if constexpr (KM == 1) {   // scale of (token, 32-channel group 2 ks + i2)
+                    const int u = 8 * n + g;
+                    const uint8_t *a = part + KC + quant::tok_sz_off(u, 2 * ks + i2, NJ);
+                    st = *reinterpret_cast<const uint16_t *>(a) * 0x10001u;
+                    zt = *reinterpret_cast<const uint16_t *>(a + 4 * NJ) * 0x10001u;
+                    if (pre) { st = hmul2_bits(st, pre); zt = hmul2_bits(zt, pre); }
+                }
+                uint32_t o[4];
+#pragma unroll
+                for (int k1 = 0; k1 < 2; ++k1)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int slot = (2 * (4 * ks + 2 * i2 + k1) + (n & 1)) * 2 + r;
+                        const uint32_t c2 = unpack<BK>(kw[n >> 1][slot / PK], slot % PK);
+                        o[2 * k1 + r] = KM == 0 ? hfma2_bits(c2, s[k1][r], z[k1][r]) : hfma2_bits(c2, st, zt);
+                    }
+                const int row = row0 + 4 * (n >> 1) + 2 * (n & 1);
+                *reinterpret_cast<uint4 *>(kt + ks * (kTile * 128) + row * 128 + (((2 * t + i2) ^ (row & 7)) << 4)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+}
+
+// Value block w of a tile -> fp16 columns of the V operand ([channel][token]); tokens from
+// `valid` on become zeros.
+template <int BV, int D>
+__device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, int w, int lane, int valid, uint32_t pre) {
+    constexpr int NJ = D / 32, KS = D / 16, PV = 16 / BV, WHV = D * BV / 64, VC = 4 * D * BV;
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t vw[2][WHV];
+    load_lane_words<WHV>(part, lane, vw[0]);
+    load_lane_words<WHV>(part + 2 * D * BV, lane, vw[1]);
+    uint32_t s[4][NJ], z[4][NJ];   // [2 kk + ch][group], a token pair each
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        const int u = 8 * n + 2 * t;
+        const uint8_t *a = part + VC + quant::tok_sz_off(u, 0, NJ);
+        if constexpr (NJ == 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(a), y = *reinterpret_cast<const uint4 *>(a + 16);
+            s[n][0] = x.x; s[n][1] = x.y; s[n][2] = x.z; s[n][3] = x.w;
+            z[n][0] = y.x; z[n][1] = y.y; z[n][2] = y.z; z[n][3] = y.w;
+        } else {
+            const uint4 x = *reinterpret_cast<const uint4 *>(a);
+            s[n][0] = x.x; s[n][1] = x.y;
+            z[n][0] = x.z; z[n][1] = x.w;
+        }
+        if (valid < 32) {   // the unused tokens' scales are not written: they may hold anything
+            const uint32_t m = (u < valid ? 0xFFFFu : 0u) | (u + 1 < valid ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) { s[n][j] &= m; z[n][j] &= m; }
+        }
+        if (pre) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) { s[n][j] = hmul2_bits(s[n][j], pre); z[n][j] = hmul2_bits(z[n][j], pre); }
+        }
+    }
+    uint8_t *base = vt + (w >> 1) * (D * 128) + (((2 * t + (w & 1)) ^ g) << 4);
+#pragma unroll
+    for (int m = 0; m < KS; ++m)
+#pragma unroll
+        for (int rh = 0; rh < 2; ++rh) {
+            uint32_t o[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int slot = 4 * m + 2 * (n & 1) + rh;
+                o[n] = hfma2_bits(unpack<BV>(vw[n >> 1][slot / PV], slot % PV), s[n][m / 2], z[n][m / 2]);
+            }
+            *reinterpret_cast<uint4 *>(base + (16 * m + 8 * rh + g) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+}
+
+// One packed value of token u, channel d of a value part, as float.
+__device__ __forceinline__ float value_at(const uint8_t *part, int u, int d, int D, int bits) {
+    int word, bit;
+    quant::code_place(1, u & 15, d, D, bits, word, bit);
+    const uint32_t w = reinterpret_cast<const uint32_t *>(part + (u >> 4) * 2 * D * bits)[word];
+    const uint8_t *sz = part + 4 * D * bits + quant::tok_sz_off(u, d >> 5, D / 32);
+    return fmaf(static_cast<float>((w >> bit) & ((1u << bits) - 1u)), __half2float(*reinterpret_cast<const __half *>(sz)),
+                __half2float(*reinterpret_cast<const __half *>(sz + 4 * (D / 32))));
+}
+
+// Byte offset of channel chunk c8 (8 channels d = 8 c8 ..) of `row` in a K-major operand whose
+// channels are permuted: the chunk's pair t goes to word 4 t' of the row (see the top); this is
+// the offset of pair 0, pair t is 32 bytes of row further before the swizzle.
+__device__ __forceinline__ int permuted_pair(int row, int c8, int t) {
+    // d = 8 c8 + 2 t: ks = c8 / 8, i = (c8 / 4) % 2, k = (c8 / 2) % 2, r = c8 % 2
+    const int chunk = 2 * t + ((c8 >> 2) & 1);
+    return (c8 >> 3) * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4) + ((c8 >> 1) & 1) * 8 + (c8 & 1) * 4;
+}
+
+// Row of 8 * NL channels held by NL lanes (8 bf16 channels each): scaled by a power of two to
+// a largest magnitude in [2^14, 2^15) and written as fp16; returns the inverse scale.
+template <int NL>
+__device__ __forceinline__ float store_scaled_row(uint8_t *tile, int row, int c8, const uint4 &x, float sign) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float f[8], mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        mx = fmaxf(mx, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
+    }
+#pragma unroll
+    for (int o = 1; o < NL; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // exponent of the largest (kept above -112 so that the inverse scale is a normal number);
+    // two exact factors, since the values are first scaled to about one
+    const int e = mx > 0.f ? max(-112, min(127, floor_log2(mx))) : 14;
+    const int a = (14 - e) / 2, b = 14 - e - a;
+    const float fa = pow2f(a) * sign, fb = pow2f(b);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        *reinterpret_cast<uint32_t *>(tile + permuted_pair(row, c8, t)) =
+            h2_bits(__floats2half2_rn(f[2 * t] * fa * fb, f[2 * t + 1] * fa * fb));
+    return pow2f(e - 14);
+}
+
+struct Waiter {
+    bool failed = false;
+    __device__ __forceinline__ void operator()(uint64_t *bar, unsigned parity) {
+        if (!failed && !mbar_wait(bar, parity)) failed = true;   // after one expiry no wait waits again
+    }
+};
+
+// ------------------------------------------------------------------ kernel
+template <int D, bool TWO>
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+    pdl_enter();
+    using SM = TreeSmem<D, TWO>;
+    constexpr int NL = D / 8;   // 8-channel chunks of a row
+    extern __shared__ __align__(1024) uint8_t smem[];
+    TreeBars *bar = reinterpret_cast<TreeBars *>(smem + SM::bars);
+    float *rowscale = reinterpret_cast<float *>(smem + SM::rowscale);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int sp = blockIdx.x, b = blockIdx.z;
+    const int groups = gridDim.y / p.Hkv, h = blockIdx.y / groups, rg = blockIdx.y % groups;
+    constexpr int ROWS = TWO ? 256 : 128;
+    const int row0 = rg * ROWS;                               // first query row (t G + g) of this CTA
+    const int nq = p.len.queries(b), L = p.len.len(b);
+    const int nrow = min(ROWS, nq * p.G - row0);              // live rows
+    if (nrow <= 0) return;
+    const int Hq = p.Hkv * p.G;
+    const long long unit = static_cast<long long>(b) * p.Hkv + h;
+    const int *depth = p.depth ? p.depth + static_cast<long long>(b) * p.T : nullptr;
+    auto row_t = [&](int r) { return (row0 + r) / p.G; };
+
+    if (tid == 0) {
+        mbar_init(&bar->q_full, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar->k_full[i], 4);
+            mbar_init(&bar->k_free[i], 1);
+            mbar_init(&bar->v_full[i], 4);
+            mbar_init(&bar->v_free[i], 1);
+            mbar_init(&bar->s_full[i], 1);
+            mbar_init(&bar->p_full[i], 4);
+            mbar_init(&bar->o_full[i], 1);
+        }
+        bar->bad_value = 0;
+        bar->min_pos = 0x7FFFFFFF;
+        fence_mbar_init();
+    }
+    if (warp == 16) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bar->tmem)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = bar->tmem;
+    // query positions; the earliest one's window bounds the tiles
+    auto query_pos = [&](int r) { return L + p.pos0 + (p.kd ? (depth ? depth[row_t(r)] : row_t(r)) : 0); };
+    if (p.window) {
+        if (tid < nrow) atomicMin(&bar->min_pos, query_pos(tid));
+        __syncthreads();
+    }
+    // open keys: the per-channel residual, then drafted tokens (a chunk: those up to the last row)
+    const int open = p.kmode == 0 ? L & 31 : 0;
+    const int nk = !p.kd ? 0 : (p.mask ? nq : min(nq, row_t(nrow - 1) + 1));
+    const int n_open = (open + nk + kTile - 1) / kTile;
+    const int nblk = (L - open + 31) >> 5;                    // packed blocks
+    int tile_first = 0;
+    if (p.window) {
+        const long long lo = static_cast<long long>(bar->min_pos) - p.window + 1;
+        if (lo > 0) tile_first = static_cast<int>(min(lo, static_cast<long long>(L)) / kTile);
+    }
+    const int n_main = max(0, (nblk + 3) / 4 - tile_first);
+    // this split's even part of the tiles: [tb, te), open tiles first
+    const int n_all = n_open + n_main;
+    const int tb = static_cast<int>(static_cast<long long>(n_all) * sp / p.S);
+    const int te = static_cast<int>(static_cast<long long>(n_all) * (sp + 1) / p.S);
+    const int n = te - tb;
+    Waiter wait;
+
+    // exact power of two that keeps the layer's cached values inside fp16 (1 for any layer whose
+    // scales are below 2^13 / (2^b - 1))
+    auto pre_exp = [&](int which, int bits) {
+        const float sm = __half2float(__ushort_as_half(static_cast<unsigned short>(p.smax[which])));
+        const float top = sm * static_cast<float>((1 << bits) - 1);
+        return top >= 16384.f ? min(14, floor_log2(top) - 13) : 0;
+    };
+    const int ek = pre_exp(0, p.bk), ev = pre_exp(1, p.bv);
+
+    if (warp >= 8 && warp < 16 && n > 0) {
+        // ================================================================ unpack warps
+        const int w = (warp - 8) & 3;
+        const bool is_v = warp >= 12;
+        const int bits = is_v ? p.bv : p.bk;
+        const int part_bytes = 4 * D * bits + 4 * D;
+        const int part_off = is_v ? 4 * D * p.bk + 4 * D : 0;
+        const int depth_r = is_v ? p.dv : p.dk;
+        const long long rec_bytes = 4LL * D * (p.bk + p.bv) + 8 * D;
+        uint8_t *ring = smem + SM::ring + (is_v ? 4 * p.dk * (4 * D * p.bk + 4 * D) : 0) + w * depth_r * part_bytes;
+        const uint32_t ring_s = smem_u32(ring);
+        auto issue = [&](int i) {   // tile tb + i into stage i % depth
+            const int ti = tb + i - n_open;
+            const int blk = 4 * (tile_first + ti) + w;
+            if (i < n && ti >= 0 && blk < nblk) {
+                const uint8_t *src = p.rec + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk) * rec_bytes + part_off;
+                const uint32_t dst = ring_s + (i % depth_r) * part_bytes;
+                for (int c = lane; c < part_bytes / 16; c += 32) cp16(dst + c * 16, src + c * 16);
+            }
+            cp_commit();
+        };
+        for (int i = 0; i < depth_r; ++i) issue(i);
+        // query rows: warp w8 of 8 takes rows w8, w8 + 8, .. pairwise (two for D = 128, four for 64)
+        {
+            constexpr int RPW = 32 / NL;
+            const float sign = p.scale < 0.f ? -1.f : 1.f;
+            const float base = fabsf(p.scale) * kLog2eT * pow2f(ek);
+            const int c8 = lane % NL;
+            for (int r0 = (warp - 8) * RPW; r0 < ROWS; r0 += 8 * RPW) {
+                const int r = r0 + lane / NL;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (r < nrow) {
+                    const int t = row_t(r), g = (row0 + r) - t * p.G;
+                    x = *reinterpret_cast<const uint4 *>(p.q + ((static_cast<long long>(b) * p.T + t) * Hq + h * p.G + g) * D +
+                                                         8 * c8);
+                }
+                const float inv = store_scaled_row<NL>(smem + SM::q + (r >> 7) * SM::OPER, r & 127, c8, x, sign);
+                if (c8 == 0) rowscale[r] = base * inv;
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->q_full);
+        }
+        const uint32_t pre = (is_v ? ev : ek) ? h2_bits(__float2half2_rn(pow2f(-(is_v ? ev : ek)))) : 0u;
+        uint64_t *full = is_v ? bar->v_full : bar->k_full, *free_ = is_v ? bar->v_free : bar->k_free;
+        for (int i = 0; i < n; ++i) {
+            const int st = i & 1;
+            uint8_t *tile = smem + (is_v ? SM::v : SM::k) + st * SM::OPER;
+            cp_wait(depth_r - 1);
+            __syncwarp();
+            if (i >= 2) wait(&free_[st], ((i >> 1) - 1) & 1);
+            const int ti = tb + i - n_open;
+            if (ti >= 0) {
+                const int blk = 4 * (tile_first + ti) + w;
+                const uint8_t *part = ring + (i % depth_r) * part_bytes;
+                if (blk < nblk) {
+                    if (!is_v) {
+                        if (p.kmode == 0) {
+                            if (bits == 8) unpack_keys<8, 0, D>(part, tile, w, lane, pre);
+                            else if (bits == 4) unpack_keys<4, 0, D>(part, tile, w, lane, pre);
+                            else unpack_keys<2, 0, D>(part, tile, w, lane, pre);
+                        } else {
+                            if (bits == 8) unpack_keys<8, 1, D>(part, tile, w, lane, pre);
+                            else if (bits == 4) unpack_keys<4, 1, D>(part, tile, w, lane, pre);
+                            else unpack_keys<2, 1, D>(part, tile, w, lane, pre);
+                        }
+                    } else {
+                        const int valid = min(32, L - 32 * blk);
+                        if (bits == 8) unpack_values<8, D>(part, tile, w, lane, valid, pre);
+                        else if (bits == 4) unpack_values<4, D>(part, tile, w, lane, valid, pre);
+                        else unpack_values<2, D>(part, tile, w, lane, valid, pre);
+                    }
+                } else if (is_v) {   // no block: its weights are zero, its values must be finite
+                    const int g = lane >> 2, t = lane & 3;
+                    for (int c = g; c < D; c += 8)
+                        *reinterpret_cast<uint4 *>(tile + (w >> 1) * (D * 128) + c * 128 + (((2 * t + (w & 1)) ^ (c & 7)) << 4)) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                }
+            } else {
+                // open tile: tokens [128 to, 128 to + 128) of (residual, drafted)
+                const int base = kTile * (tb + i);
+                const int total = open + nk;
+                if (!is_v) {
+                    float *ksc = reinterpret_cast<float *>(smem + SM::kscale) + (i & 3) * kTile;
+                    int *kp = reinterpret_cast<int *>(smem + SM::kpos) + (i & 3) * kTile;
+                    constexpr int RPW = 32 / NL;
+                    const int c8 = lane % NL;
+                    for (int r0 = 32 * w; r0 < 32 * w + 32; r0 += RPW) {
+                        const int r = r0 + lane / NL, a = base + r;
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        int pos = 0;
+                        if (a < open) {
+                            x = *reinterpret_cast<const uint4 *>(p.res + (unit * 32 + a) * D + 8 * c8);
+                            pos = (L & ~31) + a;
+                        } else if (a < total) {
+                            const int j = a - open;
+                            x = *reinterpret_cast<const uint4 *>(p.kd + (unit * p.T + j) * D + 8 * c8);
+                            pos = L + (depth ? depth[j] : j);
+                        }
+                        const float inv = store_scaled_row<NL>(tile, r, c8, x, 1.f);
+                        if (c8 == 0) {
+                            ksc[r] = inv * pow2f(-ek);   // rowscale carries 2^ek for the cached keys
+                            kp[r] = pos;
+                        }
+                    }
+                } else {
+                    // value pairs (tokens 2 j2, 2 j2 + 1 of the tile): this warp's 16 pairs
+                    const float fs = pow2f(-ev);
+                    bool bad = false;
+                    auto put = [&](int tok, int c, float v0, float v1) {
+                        *reinterpret_cast<uint32_t *>(tile + (tok >> 6) * (D * 128) + c * 128 +
+                                                      ((((tok & 63) >> 3) ^ (c & 7)) << 4) + (tok & 7) * 2) =
+                            h2_bits(__floats2half2_rn(v0, v1));
+                    };
+                    for (int it = lane; it < 16 * NL; it += 32) {
+                        const int tok = 32 * w + 2 * (it % 16), c = 8 * (it / 16);
+                        float f[2][8];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int a = base + tok + e;
+                            if (a >= open && a < total) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(p.vd + (unit * p.T + a - open) * D + c);
+                                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    float v = __uint_as_float(k & 1 ? xw[k >> 1] & 0xFFFF0000u : xw[k >> 1] << 16);
+                                    // a weight of zero must not meet NaN or infinity: those are
+                                    // added in the end, to the rows that see them
+                                    if (!(fabsf(v) < INFINITY)) { bad = true; v = 0.f; }
+                                    f[e][k] = fminf(fmaxf(v * fs, -65504.f), 65504.f);
+                                }
+                            } else if (a < open) {
+                                const uint8_t *rec = p.rec + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, L >> 5) * rec_bytes;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) f[e][k] = value_at(rec + part_off, a, c + k, D, p.bv) * fs;
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) f[e][k] = 0.f;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) put(tok, c + k, f[0][k], f[1][k]);
+                    }
+                    if (bad) bar->bad_value = 1;
+                }
             }
             __syncwarp();
+            issue(i + depth_r);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
         }
-        t0 += n;
+        cp_wait(0);
+    } else if (warp == 16) {
+        // ================================================================ MMA issue
+        if (lane == 0 && n > 0) {
+            constexpr uint32_t IQK = f16_idesc(128, kTile), IPV = f16_idesc(128, D);
+            constexpr int STEP = TWO ? 1 : 2;   // tiles from a slot's tile to its next
+            wait(&bar->q_full, 0);
+            auto qk = [&](int j, int i) {
+                const uint32_t a = smem_u32(smem + SM::q + (TWO ? j * SM::OPER : 0));
+                const uint32_t k = smem_u32(smem + SM::k + (i & 1) * SM::OPER);
+                if (!TWO || j == 0) wait(&bar->k_full[i & 1], (i >> 1) & 1);
+                fence_after();
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const int off = (s >> 2) * (kTile * 128) + (s & 3) * 32;
+                    mma_ss(tmem + j * 128, sw128_desc(a + off), sw128_desc(k + off), IQK, s > 0);
+                }
+                mma_commit(&bar->s_full[j]);
+                if (!TWO || j == 1) mma_commit(&bar->k_free[i & 1]);
+            };
+            auto pv = [&](int j, int i, int use) {
+                const uint32_t v = smem_u32(smem + SM::v + (i & 1) * SM::OPER);
+                if (!TWO || j == 0) wait(&bar->v_full[i & 1], (i >> 1) & 1);
+                wait(&bar->p_full[j], use & 1);
+                fence_after();
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                    mma_ts(tmem + 256 + j * 128, tmem + j * 128 + 8 * s, sw128_desc(v + (s >> 2) * (D * 128) + (s & 3) * 32), IPV,
+                           (use > 0 || s > 0) ? 1u : 0u);
+                if (!TWO || j == 1) mma_commit(&bar->v_free[i & 1]);
+            };
+            if (TWO) {
+                qk(0, 0);
+                qk(1, 0);
+            } else {
+                qk(0, 0);
+                if (n > 1) qk(1, 1);
+            }
+            for (int i = 0; i < n; ++i)
+                for (int j = TWO ? 0 : i & 1; j < (TWO ? 2 : (i & 1) + 1); ++j) {
+                    pv(j, i, i / STEP);
+                    if (i + STEP < n) qk(j, i + STEP);
+                    else mma_commit(&bar->o_full[j]);
+                }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ================================================================ softmax
+        const int j = warp >> 2;                    // slot
+        const int r = (TWO ? tid : tid & 127);      // row of the CTA
+        const bool live = r < nrow;
+        const bool busy = (r & ~31) < nrow;         // the warp has a live row
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + j * 128, to = tmem + lanes + 256 + j * 128;
+        const int rc = live ? r : nrow - 1;         // dead rows follow a live one
+        const int t = row_t(rc), hq = h * p.G + (row0 + rc) - t * p.G;
+        const int pos = query_pos(rc);
+        const float slope2 = p.alibi ? p.alibi[hq] * kLog2eT : 0.f;
+        const uint32_t *mrow = p.mask ? p.mask + (static_cast<long long>(b) * p.T + t) * p.mask_words : nullptr;
+        float m = -INFINITY, l = 0.f;
+        float rs = 0.f;
+        const int first = TWO ? 0 : j, step = TWO ? 1 : 2;
+        int use = 0;
+        for (int i = first; i < n; i += step, ++use) {
+            const int ti = tb + i - n_open;
+            const bool is_open = ti < 0;
+            const int base = is_open ? kTile * (tb + i) : kTile * (tile_first + ti);   // first key of the tile
+            wait(&bar->s_full[j], use & 1);
+            fence_after();
+            if (use == 0) {
+                wait(&bar->q_full, 0);
+                rs = rowscale[r];
+            }
+            if (busy) {
+                // the row's visible keys of a packed tile are tokens [lo, hi) of it
+                const int hi = min(L - open - base, kTile);
+                int lo = 0;
+                if (p.window) {
+                    const long long x = static_cast<long long>(pos) - p.window + 1 - base;
+                    lo = static_cast<int>(max(0LL, min(x, static_cast<long long>(kTile))));
+                }
+                const bool shaped = is_open || p.cap > 0.f || p.alibi ||
+                                    __any_sync(0xffffffffu, lo > 0 || hi < kTile);
+                // ---- pass 1: shape and mask (written back), row maximum in log2 units
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    ld32_issue(ts + 32 * c, x);
+                    ld32_wait(x);
+                    if (!shaped) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+                        continue;
+                    }
+                    uint32_t vis = 0xFFFFFFFFu;
+                    if (is_open) {
+                        const float *ksc = reinterpret_cast<const float *>(smem + SM::kscale) + (i & 3) * kTile + 32 * c;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * (rs * ksc[e]));
+                        // bit e: key base + 32 c + e; drafted keys j0 .. from the mask row or the chunk's rule
+                        const int j0 = base + 32 * c - open;
+                        if (j0 > -32) {
+                            uint32_t d = 0;
+                            if (mrow) {
+                                const int wi = j0 >> 5, sh = j0 & 31;   // floor: word -1 holds the residual's bits
+                                const uint32_t w0 = wi >= 0 && wi < p.mask_words ? mrow[wi] : 0u;
+                                const uint32_t w1 = wi + 1 < p.mask_words ? mrow[wi + 1] : 0u;
+                                d = __funnelshift_r(w0, w1, sh);
+                            } else {
+                                const int cnt = t + 1 - j0;
+                                d = cnt >= 32 ? 0xFFFFFFFFu : (cnt <= 0 ? 0u : (1u << cnt) - 1u);
+                            }
+                            const int end = nk - j0;   // drafted keys end here
+                            if (end < 32) d &= end <= 0 ? 0u : (1u << end) - 1u;
+                            if (j0 < 0) {              // the first -j0 keys are the residual's: seen
+                                const uint32_t resid = (1u << -j0) - 1u;
+                                d = (d & ~resid) | resid;
+                            }
+                            vis = d;
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * rs);
+                    }
+                    if (p.cap > 0.f) {
+                        // cap tanh(s / cap) = cap - 2 cap / (exp(2 s / cap) + 1), s in log2 units
+                        const float c2 = p.cap * kLog2eT, ic = 2.f / p.cap;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float ex = fast_exp2(__uint_as_float(x[e]) * ic);
+                            x[e] = __float_as_uint(fmaf(-2.f * c2, __fdividef(1.f, ex + 1.f), c2));
+                        }
+                    }
+                    if (is_open) {
+                        if (p.alibi || p.window) {
+                            const int *kp = reinterpret_cast<const int *>(smem + SM::kpos) + (i & 3) * kTile + 32 * c;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int dist = pos - kp[e];
+                                x[e] = __float_as_uint(fmaf(-slope2, static_cast<float>(dist), __uint_as_float(x[e])));
+                                if (p.window && dist >= p.window) vis &= ~(1u << e);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((vis >> e) & 1u)) x[e] = 0xFF800000u;
+                    } else {
+                        if (p.alibi) {
+                            const float d0 = static_cast<float>(pos - base - 32 * 2 * (c >> 1) - 4 * (c & 1));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)   // tile_token(32 c + e) = 64 (c / 2) + 4 (c % 2) + tile_token(e)
+                                x[e] = __float_as_uint(fmaf(-slope2, d0 - static_cast<float>(tile_token(e)), __uint_as_float(x[e])));
+                        }
+                        const int o = 64 * (c >> 1) + 4 * (c & 1);
+                        const uint32_t len = static_cast<uint32_t>(max(hi - lo, 0));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (static_cast<uint32_t>(o + tile_token(e) - lo) >= len) x[e] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+                    st32(ts + 32 * c, x);
+                }
+                if (shaped) st_wait();
+                const float f = shaped ? 1.f : rs;
+                // the maximum moves only when it grew by more than the lag, then O and l are rescaled
+                mx *= f;
+                if (__any_sync(0xffffffffu, mx > m + kLag)) {
+                    const float mn = fmaxf(m, mx);
+                    if (use > 0) {
+                        const float al = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+                        l *= al;
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t x[32];
+                            ld32_issue(to + 32 * c, x);
+                            ld32_wait(x);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * al);
+                            st32(to + 32 * c, x);
+                        }
+                    }
+                    m = mn;
+                }
+                // ---- pass 2: weights 2^(s - m + bias), their sum, fp16 into tensor memory
+                const float sub = m == -INFINITY ? 0.f : kWeightBias - m;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32], pk[16];
+                    ld32_issue(ts + 32 * c, x);
+                    ld32_wait(x);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float a = fast_exp2(fmaf(__uint_as_float(x[2 * e]), f, sub));
+                        const float d = fast_exp2(fmaf(__uint_as_float(x[2 * e + 1]), f, sub));
+                        s0 += a;
+                        s1 += d;
+                        pk[e] = pack_h2(a, d);
+                    }
+                    st16(ts + 16 * c, pk);
+                }
+                l += s0 + s1;
+                st_wait();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar->p_full[j]);
+        }
+        // ---- epilogue
+        const float vscale = pow2f(ev);
+        const bool any = first < n;
+        if (!TWO) {
+            // both slots' products are done: join them through the operand tiles
+            if (n > 0) wait(&bar->o_full[0], 0);
+            if (n > 1) wait(&bar->o_full[1], 0);
+        } else if (any) {
+            wait(&bar->o_full[j], 0);
+        }
+        fence_after();
+        float2 *mlx = reinterpret_cast<float2 *>(smem + SM::ml);
+        float other_w = 0.f, own_w = any ? 1.f : 0.f;
+        constexpr int DW = TWO ? D : D / 2;         // channels this thread writes
+        const int c0 = TWO ? 0 : j * DW;
+        float *join = reinterpret_cast<float *>(smem + SM::q);   // [2 receivers][128][kJoinRow]
+        if (!TWO) {
+            mlx[j * 128 + r] = make_float2(m, l);
+            if (any && busy) {
+                float *dst = join + ((1 - j) * 128 + r) * kJoinRow<D>;
+#pragma unroll 1
+                for (int c = 0; c < DW / 32; ++c) {
+                    uint32_t x[32];
+                    ld32_issue(to + (1 - j) * DW + 32 * c, x);
+                    ld32_wait(x);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(dst + 32 * c + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const float2 o = mlx[(1 - j) * 128 + r];
+            const float mn = fmaxf(m, o.x);
+            // (a slot without a visible key has l = 0 and O = 0; one without a tile has no O)
+            own_w = any ? (m == -INFINITY ? 1.f : fast_exp2(m - mn)) : 0.f;
+            other_w = n > 1 || j == 1 ? (o.x == -INFINITY ? 1.f : fast_exp2(o.x - mn)) : 0.f;
+            if (n == 0) other_w = 0.f;
+            l = l * own_w + o.y * other_w;
+            m = mn;
+        }
+        if (busy) {
+            const bool fix = bar->bad_value != 0;
+            const long long row = (static_cast<long long>(b) * p.T + t) * Hq + hq;
+            const bool final_ = p.S == 1;
+            const float norm = final_ ? (l == 0.f ? 0.f : vscale / l) : vscale;
+            if (!final_ && live && c0 == 0) {
+                float *ml = p.part_ml + (row * p.sstride + sp) * 2;
+                ml[0] = m;
+                ml[1] = l;
+            }
+            const float *src = join + (j * 128 + r) * kJoinRow<D>;
+#pragma unroll 1
+            for (int c = 0; c < DW / 32; ++c) {
+                uint32_t x[32];
+                __syncwarp();
+                if (any) {
+                    ld32_issue(to + c0 + 32 * c, x);
+                    ld32_wait(x);
+                }
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = any ? __uint_as_float(x[e]) * own_w : 0.f;
+                if (!TWO && other_w != 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(src + 32 * c + e);
+                        o[e] = fmaf(y.x, other_w, o[e]);
+                        o[e + 1] = fmaf(y.y, other_w, o[e + 1]);
+                        o[e + 2] = fmaf(y.z, other_w, o[e + 2]);
+                        o[e + 3] = fmaf(y.w, other_w, o[e + 3]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= norm;
+                if (fix) {
+                    // NaN or infinite drafted values of this split's open tiles, where the row sees them
+                    const int ja = max(0, kTile * tb - open), je = min(nk, kTile * min(te, n_open) - open);
+                    for (int jd = ja; jd < je; ++jd) {
+                        bool see = mrow ? (mrow[jd >> 5] >> (jd & 31)) & 1u : jd <= t;
+                        if (p.window && pos - (L + (depth ? depth[jd] : jd)) >= p.window) see = false;
+                        if (!see) continue;
+                        for (int e = 0; e < 32; ++e) {
+                            const float v = quant::bf16_to_f32(p.vd[(unit * p.T + jd) * D + c0 + 32 * c + e]);
+                            if (!(fabsf(v) < INFINITY)) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (k == e) o[k] += v;
+                            }
+                        }
+                    }
+                }
+                if (!live) {
+                    // a row behind the last drafted token: nothing is written
+                } else if (!final_) {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_acc + (row * p.sstride + sp) * D + c0 + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else if (p.out_fp32) {
+                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * D + c0 + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * D + c0 + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * e + 2 * k], o[8 * e + 2 * k + 1]);
+                            w4[k] = *reinterpret_cast<const uint32_t *>(&v);
+                        }
+                        dst[e] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    }
+                }
+            }
+        }
     }
-    for (int c = 0; c < D / 32; ++c) {
-        const float o = l == 0.f ? 0.f : acc[c] / l;
-        if (p.out_fp32) reinterpret_cast<float *>(p.out)[row * D + 32 * c + lane] = o;
-        else reinterpret_cast<__nv_bfloat16 *>(p.out)[row * D + 32 * c + lane] = __float2bfloat16_rn(o);
+    if (wait.failed) atomicOr(p.status, kStatusWaitExpired);
+    fence_before();
+    __syncthreads();
+    if (warp == 16)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// Joins the splits of every live row: a warp per row, partials in log2 units.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
+    pdl_enter();
+    const int Hq = p.Hkv * p.G, lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (row >= static_cast<long long>(p.B) * p.T * Hq) return;
+    const int b = static_cast<int>(row / Hq / p.T), t = static_cast<int>(row / Hq % p.T);
+    if (t >= p.len.queries(b)) return;
+    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + row * p.sstride;
+    float M = -INFINITY;
+    for (int s = 0; s < p.S; ++s) M = fmaxf(M, ml[s].x);
+    constexpr int PER = D / 32;
+    float o[PER], den = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int s = 0; s < p.S; ++s) {
+        const float2 v = ml[s];
+        // a split without a visible key holds zeros (or NaN and infinite values that are seen)
+        const float w = v.x == -INFINITY ? 1.f : fast_exp2(v.x - M);
+        den = fmaf(w, v.y, den);
+        const float *a = p.part_acc + (row * p.sstride + s) * D + PER * lane;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] = fmaf(w, a[e], o[e]);
+    }
+    const float n = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) {
+        const float x = o[e] * n, y = o[e + 1] * n;
+        const long long at = row * D + PER * lane + e;
+        if (p.out_fp32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(x, y);
+        else *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = __floats2bfloat162_rn(x, y);
     }
 }
+
+constexpr int kSmemMax = 232448;
+
+int part_bytes(int D, int bits) { return 4 * D * bits + 4 * D; }
+int fixed_bytes(int D, bool two) {
+    if (D == 128) return two ? TreeSmem<128, true>::ring : TreeSmem<128, false>::ring;
+    return two ? TreeSmem<64, true>::ring : TreeSmem<64, false>::ring;
+}
+// Two row tiles per CTA need 128 KB of operand tiles more than one stage of every part leaves
+// for 8-bit keys and values at head_dim 128: those run one row tile per CTA.
+bool two_tiles(int rows, int bk, int bv, int D) {
+    return rows > kTile && fixed_bytes(D, true) + 4 * (part_bytes(D, bk) + part_bytes(D, bv)) <= kSmemMax;
+}
+
+std::mutex g_tree_mu;
+bool g_tree_set[64][4];   // per device ordinal: shared-memory limits raised
 
 }  // namespace
 
-int tree_row_groups(int rows) { return (rows + 255) / 256; }
-int tree_max_splits(int, int, int) { return 1; }
+int tree_row_groups(int rows, int bk, int bv, int D) {
+    const int per = two_tiles(rows, bk, bv, D) ? 256 : 128;
+    return (rows + per - 1) / per;
+}
 
-cudaError_t launch_tree(const TreeParams &p, int D, int bk, int bv, int kmode, cudaStream_t st) {
-    const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv * p.G;
-    cudaError_t e = launch_pdl(tree_row_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, st, p, D, bk, bv,
-                               kmode);
+constexpr int kTreeSms = 148;
+
+// Partials are sized for at most four CTAs per SM.
+int tree_max_splits(int B, int Hkv, int rows) {
+    const long long ctas = static_cast<long long>(B) * Hkv * ((rows + 255) / 256);
+    return static_cast<int>(std::max(1LL, std::min(64LL, 4LL * kTreeSms / ctas)));
+}
+
+int tree_splits(int B, int Hkv, int row_groups, long long tiles, int max_splits) {
+    const long long ctas = static_cast<long long>(B) * Hkv * row_groups;
+    double best = 1e300;
+    int S = 1;
+    for (int s = 1; s <= max_splits && s <= tiles; ++s) {
+        const double waves = static_cast<double>((ctas * s + kTreeSms - 1) / kTreeSms);
+        const double cost = waves * (static_cast<double>((tiles + s - 1) / s) + 4.0) + (s > 1 ? 2.0 : 0.0);
+        if (cost < best - 1e-9) {
+            best = cost;
+            S = s;
+        }
+    }
+    return S;
+}
+
+cudaError_t launch_tree(const TreeParams &p0, int D, cudaStream_t st) {
+    TreeParams p = p0;
+    const int rows = p.T * p.G;
+    const bool two = two_tiles(rows, p.bk, p.bv, D);
+    const int groups = tree_row_groups(rows, p.bk, p.bv, D);
+    // stages of the packed parts: as many as fit, up to four, the fewer-staged kind first
+    const int pk = part_bytes(D, p.bk), pv = part_bytes(D, p.bv), fixed = fixed_bytes(D, two);
+    p.dk = p.dv = 1;
+    for (bool more = true; more;) {
+        more = false;
+        int *x = p.dk <= p.dv ? &p.dk : &p.dv;
+        for (int k = 0; k < 2 && !more; ++k, x = x == &p.dk ? &p.dv : &p.dk) {
+            if (*x >= 4) continue;
+            ++*x;
+            if (fixed + 4 * (p.dk * pk + p.dv * pv) <= kSmemMax) more = true;
+            else --*x;
+        }
+    }
+    const int smem = std::max(fixed + 4 * (p.dk * pk + p.dv * pv), 120 * 1024);   // one CTA per SM (its 512 TMEM columns)
+    using Fn = void (*)(const TreeParams);
+    const Fn fn = D == 128 ? (two ? tree_kernel<128, true> : tree_kernel<128, false>)
+                           : (two ? tree_kernel<64, true> : tree_kernel<64, false>);
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lk(g_tree_mu);
+        const int slot = (D == 128 ? 2 : 0) + (two ? 1 : 0);
+        if (dev >= 64 || !g_tree_set[dev][slot]) {
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) g_tree_set[dev][slot] = true;
+        }
+    }
+    cudaError_t e = launch_pdl(fn, dim3(p.S, p.Hkv * groups, p.B), dim3(kTreeThreads), smem, st, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-cudaError_t launch_tree_merge(const TreeParams &, int, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_tree_merge(const TreeParams &p, int D, cudaStream_t st) {
+    const long long rows = static_cast<long long>(p.B) * p.T * p.Hkv * p.G;
+    const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
+    cudaError_t e = D == 128 ? launch_pdl(tree_merge_kernel<128>, grid, dim3(256), 0, st, p)
+                             : launch_pdl(tree_merge_kernel<64>, grid, dim3(256), 0, st, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 }  // namespace kvq
