@@ -5,27 +5,30 @@
 //   s = scale q.k^,  s = cap tanh(s / cap),  s -= slope (pos_q - pos_k);  out = softmax(s) v^
 //
 // The T * G query rows that share a kv head form row tiles of 128.  A CTA (one per SM) runs a
-// part of one unit's keys against one row tile, or two (TWO): each packed block is then
-// unpacked once for up to 256 rows.  Roles:
-//   warps 0-7   softmax: two slots of 128 threads, a thread per query row.  TWO: slot j has
-//               row tile j; otherwise both slots have the one row tile and take the key tiles
-//               in turn (even, odd), each with its own sums, joined at the end.
+// part of one unit's keys against its rows.  Roles:
+//   warps 0-7   softmax: two slots of 128 threads, a thread per row of the slot's score tile.
 //   warps 8-15  unpack: warp 8 + w writes key block w (of 4) of each 128-token tile as fp16
 //               code * scale + zero, warp 12 + w the value block; packed parts come through
-//               the warp's own ring of cp.async stages.
+//               the warp's own ring of bulk copies.
 //   warp 16     one thread issues the MMAs: S = Q K^T (operands in shared memory), O += P V
 //               (P in tensor memory over S's first columns).
 // While one slot is in its softmax the other's MMAs run.
 //
-// Tiles.  First the "open" ones, keys that are bf16: the open per-channel key group (bf16
-// residual, values from its packed block), then the drafted tokens.  Then the whole packed
-// blocks, four to a tile.  Every operand is fp16 in the 128-byte-swizzled K-major layout.
-// The channel order inside a key or query row and the token order inside a tile are permuted
-// (both operands of a product alike) so that a lane's unpacked pairs are one 16-byte store
-// without bank conflicts:
+// Rows and slots.  More than 128 rows (TWO): slot j has row tile j, so each packed block is
+// unpacked once for up to 256 rows.  Otherwise both slots have the same rows and take the key
+// tiles in turn.  Up to 64 or 32 rows fill the 128 lanes as REP = 2 or 4 copies; copy c
+// weighs columns [c, c + 1) * 128 / REP of each tile (its other weights are zero), so all
+// warps share the softmax.  Slots and copies keep their own m, l and O and are joined at the
+// end.
+//
+// Tiles.  First the "open" ones, keys that are bf16: 32 places for the open per-channel key
+// group, if there is one (bf16 residual; its values are packed), then the drafted tokens.  Then
+// the whole packed blocks.  Four 32-token blocks to a tile, every operand fp16 in the
+// 128-byte-swizzled K-major layout.  The channel order inside a key or query row and the token
+// order inside a tile are permuted (both operands of a product alike) so that a lane's
+// unpacked pairs are one 16-byte store without bank conflicts:
 //   channel d = 64 ks + 32 i + 16 k + 8 r + 2 t + hb  ->  64 ks + 16 t + 8 i + 4 k + 2 r + hb
 //   token u of block w: u = 16 kk + 8 ch + 2 t + hb   ->  64 (w / 2) + 16 t + 8 (w % 2) + 4 kk + 2 ch + hb
-// (the open tiles keep their tokens in order).
 //
 // Roundings.  A cached key or value is one fp16 FMA of its exact code: off by 2^-11 of itself
 // at most, and exact where the scale and zero are subnormal.  Query rows and bf16 key rows are
@@ -136,39 +139,62 @@ struct TreeSmem {
     // keys are written, tile i - 2's scores are done, so tile i - 4's softmax is)
     static constexpr int kscale = rowscale + 256 * 4;
     static constexpr int kpos = kscale + 4 * kTile * 4;
-    static constexpr int ml = kpos + 4 * kTile * 4;             // [2][128] (m, l) to join the slots
-    static constexpr int bars = ml + (TWO ? 0 : 2 * kTile * 8); // barriers, TMEM address, flags
-    static constexpr int ring = bars + 256;                     // packed parts
+    static constexpr int bars = kpos + 4 * kTile * 4;           // barriers, TMEM address, flags
+    static constexpr int ring = bars + 512;                     // packed parts
+    // the end: (m, l) of the 256 softmax threads over the row scales .. positions, and their O
+    // rows (D + 4 floats) over the operand tiles
+    static constexpr int ml = rowscale;
+    static constexpr int ROW = D + 4;
+    static_assert(256 * ROW * 4 <= rowscale && ml + 256 * 8 <= bars, "the joining areas fit");
 };
-// Joining two slots (one row tile): each hands half its channels over, rows of D / 2 + 4 floats
-// in the operand tiles (free by then).
-template <int D>
-constexpr int kJoinRow = D / 2 + 4;
-static_assert(2 * kTile * kJoinRow<128> * 4 <= TreeSmem<128, false>::v, "the join area is the query and key tiles");
-static_assert(2 * kTile * kJoinRow<64> * 4 <= TreeSmem<64, false>::v, "the join area is the query and key tiles");
 
 struct TreeBars {
     uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2];
+    uint64_t part_full[8][4];   // packed parts, per unpack warp and stage
     uint32_t tmem, bad_value;
     int min_pos;
 };
-static_assert(sizeof(TreeBars) <= 256, "barrier area");
+static_assert(sizeof(TreeBars) <= 512, "barrier area");
 
-// Position of token `col` of a packed tile within the tile's 128 tokens.
+// Token of column `col` of a tile, and the column of token u of block w.
 __host__ __device__ constexpr int tile_token(int col) {
     return 32 * (2 * (col >> 6) + ((col >> 3) & 1)) + 16 * ((col >> 2) & 1) + 8 * ((col >> 1) & 1) + 2 * ((col >> 4) & 3) +
            (col & 1);
 }
-
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+__host__ __device__ constexpr int tile_col(int w, int u) {
+    return 64 * (w >> 1) + 16 * ((u >> 1) & 3) + 8 * (w & 1) + 4 * (u >> 4) + 2 * ((u >> 3) & 1) + (u & 1);
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait(int pending) {   // at most `pending` groups still in flight
-    if (pending == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t hfma2_bits(uint32_t c, uint32_t s, uint32_t z) {
@@ -185,8 +211,10 @@ __device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, in
     uint32_t kw[2][WHK];
     load_lane_words<WHK>(part, lane, kw[0]);
     load_lane_words<WHK>(part + 2 * D * BK, lane, kw[1]);
-    // row of token u = 16 kk + 8 i + g, n = 2 kk + i: row0 + 4 kk + 2 i
-    const int row0 = 64 * (w >> 1) + 16 * (g >> 1) + 8 * (w & 1) + (g & 1);
+    // row of token u = 16 kk + 8 i + g, n = 2 kk + i: row0 + 4 kk + 2 i; its 16-byte chunk
+    // 2 t + i2 is XOR-ed with the row's low bits (g & 1) + 4 kk + 2 i: all but the lane's own
+    // part is constant
+    const uint32_t at0 = smem_u32(kt) + tile_col(w, g) * 128 + (((2 * t) ^ (g & 1)) << 4);
 #pragma unroll
     for (int ks = 0; ks < D / 64; ++ks)
 #pragma unroll
@@ -222,9 +250,8 @@ __device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, in
                         const uint32_t c2 = unpack<BK>(kw[n >> 1][slot / PK], slot % PK);
                         o[2 * k1 + r] = KM == 0 ? hfma2_bits(c2, s[k1][r], z[k1][r]) : hfma2_bits(c2, st, zt);
                     }
-                const int row = row0 + 4 * (n >> 1) + 2 * (n & 1);
-                *reinterpret_cast<uint4 *>(kt + ks * (kTile * 128) + row * 128 + (((2 * t + i2) ^ (row & 7)) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
+                const int low = 4 * (n >> 1) + 2 * (n & 1);
+                sts128((at0 ^ ((low ^ i2) << 4)) + ks * (kTile * 128) + low * 128, o[0], o[1], o[2], o[3]);
             }
         }
 }
@@ -262,7 +289,7 @@ __device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, 
             for (int j = 0; j < NJ; ++j) { s[n][j] = hmul2_bits(s[n][j], pre); z[n][j] = hmul2_bits(z[n][j], pre); }
         }
     }
-    uint8_t *base = vt + (w >> 1) * (D * 128) + (((2 * t + (w & 1)) ^ g) << 4);
+    const uint32_t base = smem_u32(vt) + (w >> 1) * (D * 128) + g * 128 + (((2 * t + (w & 1)) ^ g) << 4);
 #pragma unroll
     for (int m = 0; m < KS; ++m)
 #pragma unroll
@@ -273,18 +300,8 @@ __device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, 
                 const int slot = 4 * m + 2 * (n & 1) + rh;
                 o[n] = hfma2_bits(unpack<BV>(vw[n >> 1][slot / PV], slot % PV), s[n][m / 2], z[n][m / 2]);
             }
-            *reinterpret_cast<uint4 *>(base + (16 * m + 8 * rh + g) * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+            sts128(base + (16 * m + 8 * rh) * 128, o[0], o[1], o[2], o[3]);
         }
-}
-
-// One packed value of token u, channel d of a value part, as float.
-__device__ __forceinline__ float value_at(const uint8_t *part, int u, int d, int D, int bits) {
-    int word, bit;
-    quant::code_place(1, u & 15, d, D, bits, word, bit);
-    const uint32_t w = reinterpret_cast<const uint32_t *>(part + (u >> 4) * 2 * D * bits)[word];
-    const uint8_t *sz = part + 4 * D * bits + quant::tok_sz_off(u, d >> 5, D / 32);
-    return fmaf(static_cast<float>((w >> bit) & ((1u << bits) - 1u)), __half2float(*reinterpret_cast<const __half *>(sz)),
-                __half2float(*reinterpret_cast<const __half *>(sz + 4 * (D / 32))));
 }
 
 // Byte offset of channel chunk c8 (8 channels d = 8 c8 ..) of `row` in a K-major operand whose
@@ -330,18 +347,21 @@ struct Waiter {
 };
 
 // ------------------------------------------------------------------ kernel
-template <int D, bool TWO>
+template <int D, bool TWO, int REP>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
     pdl_enter();
     using SM = TreeSmem<D, TWO>;
-    constexpr int NL = D / 8;   // 8-channel chunks of a row
+    constexpr int NL = D / 8;                                 // 8-channel chunks of a row
+    constexpr int COPY = kTile / REP;                         // query rows of a score tile
+    constexpr int ROWS = TWO ? 256 : COPY;                    // query rows of the CTA
+    constexpr int NC = 4 / REP;                               // 32-column chunks that a row weighs
+    static_assert(!TWO || REP == 1, "two row tiles have no copies");
     extern __shared__ __align__(1024) uint8_t smem[];
     TreeBars *bar = reinterpret_cast<TreeBars *>(smem + SM::bars);
     float *rowscale = reinterpret_cast<float *>(smem + SM::rowscale);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int sp = blockIdx.x, b = blockIdx.z;
     const int groups = gridDim.y / p.Hkv, h = blockIdx.y / groups, rg = blockIdx.y % groups;
-    constexpr int ROWS = TWO ? 256 : 128;
     const int row0 = rg * ROWS;                               // first query row (t G + g) of this CTA
     const int nq = p.len.queries(b), L = p.len.len(b);
     const int nrow = min(ROWS, nq * p.G - row0);              // live rows
@@ -362,6 +382,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             mbar_init(&bar->p_full[i], 4);
             mbar_init(&bar->o_full[i], 1);
         }
+        for (int i = 0; i < 32; ++i) mbar_init(&bar->part_full[i >> 2][i & 3], 1);
         bar->bad_value = 0;
         bar->min_pos = 0x7FFFFFFF;
         fence_mbar_init();
@@ -381,10 +402,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         if (tid < nrow) atomicMin(&bar->min_pos, query_pos(tid));
         __syncthreads();
     }
-    // open keys: the per-channel residual, then drafted tokens (a chunk: those up to the last row)
-    const int open = p.kmode == 0 ? L & 31 : 0;
+    // open keys: places for the open key group, then drafted tokens (a chunk: those up to the
+    // last row)
+    const int open = p.kmode == 0 ? L & 31 : 0, pad = open ? 32 : 0;
     const int nk = !p.kd ? 0 : (p.mask ? nq : min(nq, row_t(nrow - 1) + 1));
-    const int n_open = (open + nk + kTile - 1) / kTile;
+    const int n_open = (pad + nk + kTile - 1) / kTile;
     const int nblk = (L - open + 31) >> 5;                    // packed blocks
     int tile_first = 0;
     if (p.window) {
@@ -400,7 +422,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     Waiter wait;
 
     // exact power of two that keeps the layer's cached values inside fp16 (1 for any layer whose
-    // scales are below 2^13 / (2^b - 1))
+    // scales are below 2^14 / (2^b - 1))
     auto pre_exp = [&](int which, int bits) {
         const float sm = __half2float(__ushort_as_half(static_cast<unsigned short>(p.smax[which])));
         const float top = sm * static_cast<float>((1 << bits) - 1);
@@ -415,23 +437,29 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const int bits = is_v ? p.bv : p.bk;
         const int part_bytes = 4 * D * bits + 4 * D;
         const int part_off = is_v ? 4 * D * p.bk + 4 * D : 0;
-        const int depth_r = is_v ? p.dv : p.dk;
+        const int stages = is_v ? p.dv : p.dk;
         const long long rec_bytes = 4LL * D * (p.bk + p.bv) + 8 * D;
-        uint8_t *ring = smem + SM::ring + (is_v ? 4 * p.dk * (4 * D * p.bk + 4 * D) : 0) + w * depth_r * part_bytes;
-        const uint32_t ring_s = smem_u32(ring);
-        auto issue = [&](int i) {   // tile tb + i into stage i % depth
+        uint8_t *ring = smem + SM::ring + (is_v ? 4 * p.dk * (4 * D * p.bk + 4 * D) : 0) + w * stages * part_bytes;
+        uint64_t *part_full = bar->part_full[warp - 8];
+        // packed block of this warp in tile tb + i, or -1: the open group has packed values only
+        auto block_of = [&](int i) {
             const int ti = tb + i - n_open;
+            if (ti < 0) return is_v && pad && tb + i == 0 && w == 0 ? L >> 5 : -1;
             const int blk = 4 * (tile_first + ti) + w;
-            if (i < n && ti >= 0 && blk < nblk) {
-                const uint8_t *src = p.rec + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk) * rec_bytes + part_off;
-                const uint32_t dst = ring_s + (i % depth_r) * part_bytes;
-                for (int c = lane; c < part_bytes / 16; c += 32) cp16(dst + c * 16, src + c * 16);
-            }
-            cp_commit();
+            return blk < nblk ? blk : -1;
         };
-        for (int i = 0; i < depth_r; ++i) issue(i);
-        // query rows: warp w8 of 8 takes rows w8, w8 + 8, .. pairwise (two for D = 128, four for 64)
-        {
+        auto issue = [&](int i, int st) {
+            if (i >= n) return;
+            const int blk = block_of(i);
+            if (blk >= 0 && lane == 0) {
+                mbar_expect_tx(&part_full[st], part_bytes);
+                bulk_g2s(ring + st * part_bytes,
+                         p.rec + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk) * rec_bytes + part_off, part_bytes,
+                         &part_full[st]);
+            }
+        };
+        for (int i = 0; i < stages; ++i) issue(i, i);
+        {   // query rows, REP copies of them; two (D = 128) or four rows per warp and step
             constexpr int RPW = 32 / NL;
             const float sign = p.scale < 0.f ? -1.f : 1.f;
             const float base = fabsf(p.scale) * kLog2eT * pow2f(ek);
@@ -444,7 +472,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     x = *reinterpret_cast<const uint4 *>(p.q + ((static_cast<long long>(b) * p.T + t) * Hq + h * p.G + g) * D +
                                                          8 * c8);
                 }
-                const float inv = store_scaled_row<NL>(smem + SM::q + (r >> 7) * SM::OPER, r & 127, c8, x, sign);
+                float inv = 1.f;
+#pragma unroll
+                for (int k = 0; k < REP; ++k)
+                    inv = store_scaled_row<NL>(smem + SM::q + (r >> 7) * SM::OPER, (r & 127) + k * COPY, c8, x, sign);
                 if (c8 == 0) rowscale[r] = base * inv;
             }
             fence_proxy_async();
@@ -453,114 +484,94 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         }
         const uint32_t pre = (is_v ? ev : ek) ? h2_bits(__float2half2_rn(pow2f(-(is_v ? ev : ek)))) : 0u;
         uint64_t *full = is_v ? bar->v_full : bar->k_full, *free_ = is_v ? bar->v_free : bar->k_free;
-        for (int i = 0; i < n; ++i) {
-            const int st = i & 1;
-            uint8_t *tile = smem + (is_v ? SM::v : SM::k) + st * SM::OPER;
-            cp_wait(depth_r - 1);
-            __syncwarp();
-            if (i >= 2) wait(&free_[st], ((i >> 1) - 1) & 1);
-            const int ti = tb + i - n_open;
-            if (ti >= 0) {
-                const int blk = 4 * (tile_first + ti) + w;
-                const uint8_t *part = ring + (i % depth_r) * part_bytes;
-                if (blk < nblk) {
-                    if (!is_v) {
-                        if (p.kmode == 0) {
-                            if (bits == 8) unpack_keys<8, 0, D>(part, tile, w, lane, pre);
-                            else if (bits == 4) unpack_keys<4, 0, D>(part, tile, w, lane, pre);
-                            else unpack_keys<2, 0, D>(part, tile, w, lane, pre);
-                        } else {
-                            if (bits == 8) unpack_keys<8, 1, D>(part, tile, w, lane, pre);
-                            else if (bits == 4) unpack_keys<4, 1, D>(part, tile, w, lane, pre);
-                            else unpack_keys<2, 1, D>(part, tile, w, lane, pre);
-                        }
-                    } else {
-                        const int valid = min(32, L - 32 * blk);
-                        if (bits == 8) unpack_values<8, D>(part, tile, w, lane, valid, pre);
-                        else if (bits == 4) unpack_values<4, D>(part, tile, w, lane, valid, pre);
-                        else unpack_values<2, D>(part, tile, w, lane, valid, pre);
-                    }
-                } else if (is_v) {   // no block: its weights are zero, its values must be finite
-                    const int g = lane >> 2, t = lane & 3;
-                    for (int c = g; c < D; c += 8)
-                        *reinterpret_cast<uint4 *>(tile + (w >> 1) * (D * 128) + c * 128 + (((2 * t + (w & 1)) ^ (c & 7)) << 4)) =
-                            make_uint4(0u, 0u, 0u, 0u);
-                }
-            } else {
-                // open tile: tokens [128 to, 128 to + 128) of (residual, drafted)
-                const int base = kTile * (tb + i);
-                const int total = open + nk;
-                if (!is_v) {
-                    float *ksc = reinterpret_cast<float *>(smem + SM::kscale) + (i & 3) * kTile;
-                    int *kp = reinterpret_cast<int *>(smem + SM::kpos) + (i & 3) * kTile;
-                    constexpr int RPW = 32 / NL;
-                    const int c8 = lane % NL;
-                    for (int r0 = 32 * w; r0 < 32 * w + 32; r0 += RPW) {
-                        const int r = r0 + lane / NL, a = base + r;
-                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        int pos = 0;
-                        if (a < open) {
-                            x = *reinterpret_cast<const uint4 *>(p.res + (unit * 32 + a) * D + 8 * c8);
-                            pos = (L & ~31) + a;
-                        } else if (a < total) {
-                            const int j = a - open;
-                            x = *reinterpret_cast<const uint4 *>(p.kd + (unit * p.T + j) * D + 8 * c8);
-                            pos = L + (depth ? depth[j] : j);
-                        }
-                        const float inv = store_scaled_row<NL>(tile, r, c8, x, 1.f);
-                        if (c8 == 0) {
-                            ksc[r] = inv * pow2f(-ek);   // rowscale carries 2^ek for the cached keys
-                            kp[r] = pos;
-                        }
-                    }
-                } else {
-                    // value pairs (tokens 2 j2, 2 j2 + 1 of the tile): this warp's 16 pairs
-                    const float fs = pow2f(-ev);
-                    bool bad = false;
-                    auto put = [&](int tok, int c, float v0, float v1) {
-                        *reinterpret_cast<uint32_t *>(tile + (tok >> 6) * (D * 128) + c * 128 +
-                                                      ((((tok & 63) >> 3) ^ (c & 7)) << 4) + (tok & 7) * 2) =
-                            h2_bits(__floats2half2_rn(v0, v1));
-                    };
-                    for (int it = lane; it < 16 * NL; it += 32) {
-                        const int tok = 32 * w + 2 * (it % 16), c = 8 * (it / 16);
-                        float f[2][8];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int a = base + tok + e;
-                            if (a >= open && a < total) {
-                                const uint4 x = *reinterpret_cast<const uint4 *>(p.vd + (unit * p.T + a - open) * D + c);
-                                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    float v = __uint_as_float(k & 1 ? xw[k >> 1] & 0xFFFF0000u : xw[k >> 1] << 16);
-                                    // a weight of zero must not meet NaN or infinity: those are
-                                    // added in the end, to the rows that see them
-                                    if (!(fabsf(v) < INFINITY)) { bad = true; v = 0.f; }
-                                    f[e][k] = fminf(fmaxf(v * fs, -65504.f), 65504.f);
-                                }
-                            } else if (a < open) {
-                                const uint8_t *rec = p.rec + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, L >> 5) * rec_bytes;
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) f[e][k] = value_at(rec + part_off, a, c + k, D, p.bv) * fs;
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) f[e][k] = 0.f;
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) put(tok, c + k, f[0][k], f[1][k]);
-                    }
-                    if (bad) bar->bad_value = 1;
-                }
+        uint32_t part_phase = 0;   // bit per stage
+        for (int i = 0, st = 0; i < n; ++i, st = st + 1 == stages ? 0 : st + 1) {
+            uint8_t *tile = smem + (is_v ? SM::v : SM::k) + (i & 1) * SM::OPER;
+            const int blk = block_of(i);
+            if (blk >= 0) {
+                wait(&part_full[st], (part_phase >> st) & 1u);
+                part_phase ^= 1u << st;
             }
-            __syncwarp();
-            issue(i + depth_r);
+            if (i >= 2) wait(&free_[i & 1], ((i >> 1) - 1) & 1);
+            const uint8_t *part = ring + st * part_bytes;
+            const bool is_open = tb + i < n_open;
+            const int j0 = kTile * (tb + i) + 32 * w - pad;   // open tiles: the block's first drafted token
+            if (!is_v && blk >= 0) {
+                if (p.kmode == 0) {
+                    if (bits == 8) unpack_keys<8, 0, D>(part, tile, w, lane, pre);
+                    else if (bits == 4) unpack_keys<4, 0, D>(part, tile, w, lane, pre);
+                    else unpack_keys<2, 0, D>(part, tile, w, lane, pre);
+                } else {
+                    if (bits == 8) unpack_keys<8, 1, D>(part, tile, w, lane, pre);
+                    else if (bits == 4) unpack_keys<4, 1, D>(part, tile, w, lane, pre);
+                    else unpack_keys<2, 1, D>(part, tile, w, lane, pre);
+                }
+            } else if (!is_v && is_open) {
+                // bf16 rows: the open group's, or drafted tokens (rows behind them are masked)
+                float *ksc = reinterpret_cast<float *>(smem + SM::kscale) + (i & 3) * kTile;
+                int *kp = reinterpret_cast<int *>(smem + SM::kpos) + (i & 3) * kTile;
+                constexpr int RPW = 32 / NL;
+                const int c8 = lane % NL;
+                for (int u0 = 0; u0 < 32 && (j0 < 0 || j0 + u0 < nk); u0 += RPW) {
+                    const int u = u0 + lane / NL, row = tile_col(w, u);
+                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                    int pos = 0;
+                    if (j0 < 0) {
+                        if (u < open) x = *reinterpret_cast<const uint4 *>(p.res + (unit * 32 + u) * D + 8 * c8);
+                        pos = (L & ~31) + u;
+                    } else if (j0 + u < nk) {
+                        x = *reinterpret_cast<const uint4 *>(p.kd + (unit * p.T + j0 + u) * D + 8 * c8);
+                        pos = L + (depth ? depth[j0 + u] : j0 + u);
+                    }
+                    const float inv = store_scaled_row<NL>(tile, row, c8, x, 1.f);
+                    if (c8 == 0) {
+                        ksc[row] = inv * pow2f(-ek);   // the row scale carries 2^ek for the cached keys
+                        kp[row] = pos;
+                    }
+                }
+            } else if (is_v && blk >= 0) {
+                const int valid = min(32, L - 32 * blk);
+                if (bits == 8) unpack_values<8, D>(part, tile, w, lane, valid, pre);
+                else if (bits == 4) unpack_values<4, D>(part, tile, w, lane, valid, pre);
+                else unpack_values<2, D>(part, tile, w, lane, valid, pre);
+            } else if (is_v && is_open && j0 < nk) {
+                // drafted values: token pairs (u, u + 1) of the block
+                const float fs = pow2f(-ev);
+                bool bad = false;
+                for (int it = lane; it < 16 * NL; it += 32) {
+                    const int u = 2 * (it % 16), c = 8 * (it / 16), col = tile_col(w, u);
+                    float f[2][8];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (j0 + u + e < nk) x = *reinterpret_cast<const uint4 *>(p.vd + (unit * p.T + j0 + u + e) * D + c);
+                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float v = __uint_as_float(k & 1 ? xw[k >> 1] & 0xFFFF0000u : xw[k >> 1] << 16);
+                            // a weight of zero must not meet NaN or infinity: those are added in
+                            // the end, to the rows that see them
+                            if (!(fabsf(v) < INFINITY)) { bad = true; v = 0.f; }
+                            f[e][k] = fminf(fmaxf(v * fs, -65504.f), 65504.f);
+                        }
+                    }
+                    uint8_t *at = tile + (col >> 6) * (D * 128) + c * 128 + (col & 7) * 2;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint32_t *>(at + k * 128 + ((((col & 63) >> 3) ^ k) << 4)) =
+                            h2_bits(__floats2half2_rn(f[0][k], f[1][k]));
+                }
+                if (bad) bar->bad_value = 1;
+            } else if (is_v) {   // nothing here: the weights are zero, the values must be finite
+                const int g = lane >> 2, t = lane & 3;
+                const uint32_t at = smem_u32(tile) + (w >> 1) * (D * 128) + g * 128 + (((2 * t + (w & 1)) ^ g) << 4);
+                for (int c = 0; c < D; c += 8) sts128(at + c * 128, 0u, 0u, 0u, 0u);
+            }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
+            if (lane == 0) mbar_arrive(&full[i & 1]);
+            issue(i + stages, st);
         }
-        cp_wait(0);
     } else if (warp == 16) {
         // ================================================================ MMA issue
         if (lane == 0 && n > 0) {
@@ -591,13 +602,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                            (use > 0 || s > 0) ? 1u : 0u);
                 if (!TWO || j == 1) mma_commit(&bar->v_free[i & 1]);
             };
-            if (TWO) {
-                qk(0, 0);
-                qk(1, 0);
-            } else {
-                qk(0, 0);
-                if (n > 1) qk(1, 1);
-            }
+            // MMAs of one thread run in order: a slot's next scores may overwrite the weights
+            // that its previous product reads
+            qk(0, 0);
+            if (TWO) qk(1, 0);
+            else if (n > 1) qk(1, 1);
             for (int i = 0; i < n; ++i)
                 for (int j = TWO ? 0 : i & 1; j < (TWO ? 2 : (i & 1) + 1); ++j) {
                     pv(j, i, i / STEP);
@@ -608,25 +617,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         __syncwarp();
     } else if (warp < 8) {
         // ================================================================ softmax
-        const int j = warp >> 2;                    // slot
-        const int r = (TWO ? tid : tid & 127);      // row of the CTA
-        const bool live = r < nrow;
-        const bool busy = (r & ~31) < nrow;         // the warp has a live row
+        const int j = warp >> 2;                                 // slot
+        const int r = TWO ? tid : (tid & 127) % COPY;            // query row of the CTA
+        const int copy = TWO ? 0 : (tid & 127) / COPY;
+        const bool busy = (r & ~31) < nrow;                      // the warp has a live row
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + j * 128, to = tmem + lanes + 256 + j * 128;
-        const int rc = live ? r : nrow - 1;         // dead rows follow a live one
+        const int rc = min(r, nrow - 1);                         // dead rows follow a live one
         const int t = row_t(rc), hq = h * p.G + (row0 + rc) - t * p.G;
         const int pos = query_pos(rc);
         const float slope2 = p.alibi ? p.alibi[hq] * kLog2eT : 0.f;
         const uint32_t *mrow = p.mask ? p.mask + (static_cast<long long>(b) * p.T + t) * p.mask_words : nullptr;
-        float m = -INFINITY, l = 0.f;
-        float rs = 0.f;
+        float m = -INFINITY, l = 0.f, rs = 0.f;
         const int first = TWO ? 0 : j, step = TWO ? 1 : 2;
         int use = 0;
         for (int i = first; i < n; i += step, ++use) {
             const int ti = tb + i - n_open;
             const bool is_open = ti < 0;
-            const int base = is_open ? kTile * (tb + i) : kTile * (tile_first + ti);   // first key of the tile
+            const int base = is_open ? kTile * (tb + i) : kTile * (tile_first + ti);   // first place of the tile
             wait(&bar->s_full[j], use & 1);
             fence_after();
             if (use == 0) {
@@ -641,90 +649,109 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     const long long x = static_cast<long long>(pos) - p.window + 1 - base;
                     lo = static_cast<int>(max(0LL, min(x, static_cast<long long>(kTile))));
                 }
-                const bool shaped = is_open || p.cap > 0.f || p.alibi ||
-                                    __any_sync(0xffffffffu, lo > 0 || hi < kTile);
-                // ---- pass 1: shape and mask (written back), row maximum in log2 units
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    ld32_issue(ts + 32 * c, x);
-                    ld32_wait(x);
-                    if (!shaped) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
-                        continue;
-                    }
-                    uint32_t vis = 0xFFFFFFFFu;
+                const bool cut = !is_open && __any_sync(0xffffffffu, lo > 0 || hi < kTile);
+                const bool shaped = is_open || p.cap > 0.f || p.alibi || cut;
+                // raw scores of chunk c -> log2 units, capped, biased, masked
+                auto shape = [&](uint32_t *x, int c) {
                     if (is_open) {
-                        const float *ksc = reinterpret_cast<const float *>(smem + SM::kscale) + (i & 3) * kTile + 32 * c;
+                        const float4 *ksc = reinterpret_cast<const float4 *>(smem + SM::kscale) + ((i & 3) * kTile + 32 * c) / 4;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * (rs * ksc[e]));
-                        // bit e: key base + 32 c + e; drafted keys j0 .. from the mask row or the chunk's rule
-                        const int j0 = base + 32 * c - open;
-                        if (j0 > -32) {
-                            uint32_t d = 0;
-                            if (mrow) {
-                                const int wi = j0 >> 5, sh = j0 & 31;   // floor: word -1 holds the residual's bits
-                                const uint32_t w0 = wi >= 0 && wi < p.mask_words ? mrow[wi] : 0u;
-                                const uint32_t w1 = wi + 1 < p.mask_words ? mrow[wi + 1] : 0u;
-                                d = __funnelshift_r(w0, w1, sh);
-                            } else {
-                                const int cnt = t + 1 - j0;
-                                d = cnt >= 32 ? 0xFFFFFFFFu : (cnt <= 0 ? 0u : (1u << cnt) - 1u);
-                            }
-                            const int end = nk - j0;   // drafted keys end here
-                            if (end < 32) d &= end <= 0 ? 0u : (1u << end) - 1u;
-                            if (j0 < 0) {              // the first -j0 keys are the residual's: seen
-                                const uint32_t resid = (1u << -j0) - 1u;
-                                d = (d & ~resid) | resid;
-                            }
-                            vis = d;
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 k4 = ksc[e / 4];
+                            x[e] = __float_as_uint(__uint_as_float(x[e]) * (rs * k4.x));
+                            x[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * (rs * k4.y));
+                            x[e + 2] = __float_as_uint(__uint_as_float(x[e + 2]) * (rs * k4.z));
+                            x[e + 3] = __float_as_uint(__uint_as_float(x[e + 3]) * (rs * k4.w));
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * rs);
                     }
+                    const float f = is_open ? 1.f : rs;
                     if (p.cap > 0.f) {
-                        // cap tanh(s / cap) = cap - 2 cap / (exp(2 s / cap) + 1), s in log2 units
-                        const float c2 = p.cap * kLog2eT, ic = 2.f / p.cap;
+                        // cap tanh(s / cap) = cap - 2 cap / (exp(2 s / cap) + 1), in log2 units
+                        const float c2 = p.cap * kLog2eT, fc = f * (2.f / p.cap);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            x[e] = __float_as_uint(
+                                fmaf(-2.f * c2, fast_rcp(fast_exp2(__uint_as_float(x[e]) * fc) + 1.f), c2));
+                    } else if (!is_open && !p.alibi) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+                    }
+                    const float g = p.cap > 0.f ? 1.f : f;
+                    if (is_open) {
+                        // visibility words of the chunk's two blocks; bit u: place u of the block
+                        uint32_t vis[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j0 = base + 32 * (2 * (c >> 1) + k) - pad;
+                            uint32_t d = (1u << open) - 1u;           // the open group: seen
+                            if (j0 >= 0) {
+                                if (mrow) d = (j0 >> 5) < p.mask_words ? mrow[j0 >> 5] : 0u;
+                                else d = t - j0 >= 31 ? 0xFFFFFFFFu : (t < j0 ? 0u : (2u << (t - j0)) - 1u);
+                                if (nk - j0 < 32) d &= nk <= j0 ? 0u : (1u << (nk - j0)) - 1u;
+                            }
+                            vis[k] = d >> (4 * (c & 1));
+                        }
+                        const int4 *kp = reinterpret_cast<const int4 *>(smem + SM::kpos) + ((i & 3) * kTile + 32 * c) / 4;
+                        const bool posn = p.alibi || p.window;
+                        const int far = p.window ? p.window : 0x7FFFFFFF;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const float ex = fast_exp2(__uint_as_float(x[e]) * ic);
-                            x[e] = __float_as_uint(fmaf(-2.f * c2, __fdividef(1.f, ex + 1.f), c2));
-                        }
-                    }
-                    if (is_open) {
-                        if (p.alibi || p.window) {
-                            const int *kp = reinterpret_cast<const int *>(smem + SM::kpos) + (i & 3) * kTile + 32 * c;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int dist = pos - kp[e];
+                            bool see = (vis[(e >> 3) & 1] >> (tile_token(e) & 31)) & 1u;
+                            if (posn) {
+                                const int4 k4 = kp[e / 4];
+                                const int dist = pos - ((e & 3) == 0 ? k4.x : (e & 3) == 1 ? k4.y : (e & 3) == 2 ? k4.z : k4.w);
                                 x[e] = __float_as_uint(fmaf(-slope2, static_cast<float>(dist), __uint_as_float(x[e])));
-                                if (p.window && dist >= p.window) vis &= ~(1u << e);
+                                see = see && dist < far;
                             }
+                            if (!see) x[e] = 0xFF800000u;
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((vis >> e) & 1u)) x[e] = 0xFF800000u;
                     } else {
+                        const int o = 64 * (c >> 1) + 4 * (c & 1);   // tile_token(32 c + e) = o + tile_token(e)
                         if (p.alibi) {
-                            const float d0 = static_cast<float>(pos - base - 32 * 2 * (c >> 1) - 4 * (c & 1));
+                            const float d0 = -slope2 * static_cast<float>(pos - base - o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)   // tile_token(32 c + e) = 64 (c / 2) + 4 (c % 2) + tile_token(e)
-                                x[e] = __float_as_uint(fmaf(-slope2, d0 - static_cast<float>(tile_token(e)), __uint_as_float(x[e])));
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), g,
+                                                            fmaf(slope2, static_cast<float>(tile_token(e)), d0)));
                         }
-                        const int o = 64 * (c >> 1) + 4 * (c & 1);
-                        const uint32_t len = static_cast<uint32_t>(max(hi - lo, 0));
+                        if (cut) {
+                            const uint32_t len = static_cast<uint32_t>(max(hi - lo, 0));
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (static_cast<uint32_t>(o + tile_token(e) - lo) >= len) x[e] = 0xFF800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (static_cast<uint32_t>(o + tile_token(e) - lo) >= len) x[e] = 0xFF800000u;
+                        }
                     }
+                };
+                auto top = [&](const uint32_t *x, float mx) {
+                    float a = mx, d = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
-                    st32(ts + 32 * c, x);
+                    for (int e = 0; e < 32; e += 4) {
+                        a = max3(a, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        d = max3(d, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                    }
+                    return fmaxf(a, d);
+                };
+                // ---- pass 1: row maximum (shaped scores are written back)
+                uint32_t x[32];
+                float mx = -INFINITY;
+                if (NC == 1) {
+                    ld32_issue(ts + 32 * copy, x);
+                    ld32_wait(x);
+                    if (shaped) shape(x, copy);
+                    mx = top(x, mx);
+                } else {
+#pragma unroll 1
+                    for (int c = copy * NC; c < copy * NC + NC; ++c) {
+                        ld32_issue(ts + 32 * c, x);
+                        ld32_wait(x);
+                        if (shaped) {
+                            shape(x, c);
+                            st32(ts + 32 * c, x);
+                        }
+                        mx = top(x, mx);
+                    }
+                    if (shaped) st_wait();
                 }
-                if (shaped) st_wait();
                 const float f = shaped ? 1.f : rs;
                 // the maximum moves only when it grew by more than the lag, then O and l are rescaled
                 mx *= f;
@@ -735,34 +762,53 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         l *= al;
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
-                            uint32_t x[32];
-                            ld32_issue(to + 32 * c, x);
-                            ld32_wait(x);
+                            uint32_t y[32];
+                            ld32_issue(to + 32 * c, y);
+                            ld32_wait(y);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * al);
-                            st32(to + 32 * c, x);
+                            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * al);
+                            st32(to + 32 * c, y);
                         }
                     }
                     m = mn;
                 }
                 // ---- pass 2: weights 2^(s - m + bias), their sum, fp16 into tensor memory
                 const float sub = m == -INFINITY ? 0.f : kWeightBias - m;
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32], pk[16];
-                    ld32_issue(ts + 32 * c, x);
-                    ld32_wait(x);
+                const uint64_t f2 = pack2(f, f), sub2 = pack2(sub, sub);
+                uint64_t sum = pack2(0.f, 0.f);
+                auto weigh = [&](const uint32_t *x, int c) {
+                    uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float a = fast_exp2(fmaf(__uint_as_float(x[2 * e]), f, sub));
-                        const float d = fast_exp2(fmaf(__uint_as_float(x[2 * e + 1]), f, sub));
-                        s0 += a;
-                        s1 += d;
+                        float a, d;
+                        unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2, sub2), a, d);
+                        a = fast_exp2(a);
+                        d = fast_exp2(d);
+                        sum = add2(sum, pack2(a, d));
                         pk[e] = pack_h2(a, d);
                     }
                     st16(ts + 16 * c, pk);
+                };
+                if (NC == 1) {
+                    weigh(x, copy);
+                } else {
+#pragma unroll 1
+                    for (int c = copy * NC; c < copy * NC + NC; ++c) {
+                        ld32_issue(ts + 32 * c, x);
+                        ld32_wait(x);
+                        weigh(x, c);
+                    }
                 }
+                if (REP > 1) {   // the other copies' columns
+                    uint32_t zero[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) zero[e] = 0u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (c / NC != copy) st16(ts + 16 * c, zero);
+                }
+                float s0, s1;
+                unpack2(sum, s0, s1);
                 l += s0 + s1;
                 st_wait();
             }
@@ -770,120 +816,102 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar->p_full[j]);
         }
-        // ---- epilogue
-        const float vscale = pow2f(ev);
-        const bool any = first < n;
-        if (!TWO) {
-            // both slots' products are done: join them through the operand tiles
-            if (n > 0) wait(&bar->o_full[0], 0);
-            if (n > 1) wait(&bar->o_full[1], 0);
-        } else if (any) {
-            wait(&bar->o_full[j], 0);
-        }
+        // ---- the end: join slots and copies, write rows
+        if (n > 0) wait(&bar->o_full[0], 0);
+        if (TWO ? n > 0 : n > 1) wait(&bar->o_full[1], 0);
         fence_after();
+        const bool any = first < n, final_ = p.S == 1;
+        const int slots = min(n, 2);                             // slots with a tile (one row tile)
         float2 *mlx = reinterpret_cast<float2 *>(smem + SM::ml);
-        float other_w = 0.f, own_w = any ? 1.f : 0.f;
-        constexpr int DW = TWO ? D : D / 2;         // channels this thread writes
-        const int c0 = TWO ? 0 : j * DW;
-        float *join = reinterpret_cast<float *>(smem + SM::q);   // [2 receivers][128][kJoinRow]
+        float *rows_o = reinterpret_cast<float *>(smem);
+        float own = 1.f;
         if (!TWO) {
-            mlx[j * 128 + r] = make_float2(m, l);
-            if (any && busy) {
-                float *dst = join + ((1 - j) * 128 + r) * kJoinRow<D>;
-#pragma unroll 1
-                for (int c = 0; c < DW / 32; ++c) {
-                    uint32_t x[32];
-                    ld32_issue(to + (1 - j) * DW + 32 * c, x);
-                    ld32_wait(x);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(dst + 32 * c + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-                }
-            }
+            mlx[tid] = make_float2(m, l);
             asm volatile("bar.sync 1, 256;" ::: "memory");
-            const float2 o = mlx[(1 - j) * 128 + r];
-            const float mn = fmaxf(m, o.x);
-            // (a slot without a visible key has l = 0 and O = 0; one without a tile has no O)
-            own_w = any ? (m == -INFINITY ? 1.f : fast_exp2(m - mn)) : 0.f;
-            other_w = n > 1 || j == 1 ? (o.x == -INFINITY ? 1.f : fast_exp2(o.x - mn)) : 0.f;
-            if (n == 0) other_w = 0.f;
-            l = l * own_w + o.y * other_w;
-            m = mn;
+            float M = -INFINITY;
+            for (int s = 0; s < slots; ++s)
+#pragma unroll
+                for (int k = 0; k < REP; ++k) M = fmaxf(M, mlx[s * 128 + k * COPY + r].x);
+            // (a part without a visible key has l = 0 and O = 0)
+            own = m == -INFINITY ? 1.f : fast_exp2(m - M);
+            l = 0.f;
+            for (int s = 0; s < slots; ++s)
+#pragma unroll
+                for (int k = 0; k < REP; ++k) {
+                    const float2 y = mlx[s * 128 + k * COPY + r];
+                    l += y.x == -INFINITY ? y.y : y.y * fast_exp2(y.x - M);
+                }
+            m = M;
         }
-        if (busy) {
-            const bool fix = bar->bad_value != 0;
-            const long long row = (static_cast<long long>(b) * p.T + t) * Hq + hq;
-            const bool final_ = p.S == 1;
-            const float norm = final_ ? (l == 0.f ? 0.f : vscale / l) : vscale;
-            if (!final_ && live && c0 == 0) {
-                float *ml = p.part_ml + (row * p.sstride + sp) * 2;
-                ml[0] = m;
-                ml[1] = l;
-            }
-            const float *src = join + (j * 128 + r) * kJoinRow<D>;
+        if (busy && any) {
+            own *= pow2f(ev) * (final_ ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+            float *dst = rows_o + tid * SM::ROW;
 #pragma unroll 1
-            for (int c = 0; c < DW / 32; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
                 uint32_t x[32];
-                __syncwarp();
-                if (any) {
-                    ld32_issue(to + c0 + 32 * c, x);
-                    ld32_wait(x);
-                }
-                float o[32];
+                ld32_issue(to + 32 * c, x);
+                ld32_wait(x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = any ? __uint_as_float(x[e]) * own_w : 0.f;
-                if (!TWO && other_w != 0.f) {
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4 *>(dst + 32 * c + e) =
+                        make_float4(__uint_as_float(x[e]) * own, __uint_as_float(x[e + 1]) * own,
+                                    __uint_as_float(x[e + 2]) * own, __uint_as_float(x[e + 3]) * own);
+            }
+        }
+        if (!final_ && r < nrow && copy == 0 && (TWO || j == 0))
+            *reinterpret_cast<float2 *>(p.part_ml + (((static_cast<long long>(b) * p.T + t) * Hq + hq) * p.sstride + sp) * 2) =
+                make_float2(m, l);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const bool fix = bar->bad_value != 0;
+        for (int it = tid; it < nrow * NL; it += 256) {
+            const int rr = it / NL, c = 8 * (it % NL);
+            const int tt = row_t(rr), hh = h * p.G + (row0 + rr) - tt * p.G;
+            float o[8];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(src + 32 * c + e);
-                        o[e] = fmaf(y.x, other_w, o[e]);
-                        o[e + 1] = fmaf(y.y, other_w, o[e + 1]);
-                        o[e + 2] = fmaf(y.z, other_w, o[e + 2]);
-                        o[e + 3] = fmaf(y.w, other_w, o[e + 3]);
+            for (int e = 0; e < 8; ++e) o[e] = 0.f;
+            auto add = [&](int src) {
+                const float4 x = *reinterpret_cast<const float4 *>(rows_o + src * SM::ROW + c);
+                const float4 y = *reinterpret_cast<const float4 *>(rows_o + src * SM::ROW + c + 4);
+                o[0] += x.x; o[1] += x.y; o[2] += x.z; o[3] += x.w;
+                o[4] += y.x; o[5] += y.y; o[6] += y.z; o[7] += y.w;
+            };
+            if (TWO) {
+                if (n > 0) add(rr);
+            } else {
+                for (int s = 0; s < slots; ++s)
+#pragma unroll
+                    for (int k = 0; k < REP; ++k) add(s * 128 + k * COPY + rr);
+            }
+            if (fix) {
+                // NaN and infinite drafted values of this split's open tiles, where the row sees them
+                const uint32_t *mr = p.mask ? p.mask + (static_cast<long long>(b) * p.T + tt) * p.mask_words : nullptr;
+                const int qp = query_pos(rr);
+                const int ja = max(0, kTile * tb - pad), je = min(nk, kTile * min(te, n_open) - pad);
+                for (int jd = ja; jd < je; ++jd) {
+                    bool see = mr ? (mr[jd >> 5] >> (jd & 31)) & 1u : jd <= tt;
+                    if (p.window && qp - (L + (depth ? depth[jd] : jd)) >= p.window) see = false;
+                    if (!see) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = quant::bf16_to_f32(p.vd[(unit * p.T + jd) * D + c + e]);
+                        if (!(fabsf(v) < INFINITY)) o[e] += v;
                     }
                 }
+            }
+            const long long row = (static_cast<long long>(b) * p.T + tt) * Hq + hh;
+            if (!final_ || p.out_fp32) {
+                float *dst = final_ ? static_cast<float *>(p.out) + row * D + c
+                                    : p.part_acc + (row * p.sstride + sp) * D + c;
+                reinterpret_cast<float4 *>(dst)[0] = make_float4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<float4 *>(dst)[1] = make_float4(o[4], o[5], o[6], o[7]);
+            } else {
+                uint32_t w4[4];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= norm;
-                if (fix) {
-                    // NaN or infinite drafted values of this split's open tiles, where the row sees them
-                    const int ja = max(0, kTile * tb - open), je = min(nk, kTile * min(te, n_open) - open);
-                    for (int jd = ja; jd < je; ++jd) {
-                        bool see = mrow ? (mrow[jd >> 5] >> (jd & 31)) & 1u : jd <= t;
-                        if (p.window && pos - (L + (depth ? depth[jd] : jd)) >= p.window) see = false;
-                        if (!see) continue;
-                        for (int e = 0; e < 32; ++e) {
-                            const float v = quant::bf16_to_f32(p.vd[(unit * p.T + jd) * D + c0 + 32 * c + e]);
-                            if (!(fabsf(v) < INFINITY)) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (k == e) o[k] += v;
-                            }
-                        }
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
+                    w4[k] = *reinterpret_cast<const uint32_t *>(&v);
                 }
-                if (!live) {
-                    // a row behind the last drafted token: nothing is written
-                } else if (!final_) {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_acc + (row * p.sstride + sp) * D + c0 + 32 * c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else if (p.out_fp32) {
-                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * D + c0 + 32 * c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * D + c0 + 32 * c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w4[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * e + 2 * k], o[8 * e + 2 * k + 1]);
-                            w4[k] = *reinterpret_cast<const uint32_t *>(&v);
-                        }
-                        dst[e] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                    }
-                }
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.out) + row * D + c) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
         }
     }
@@ -943,7 +971,7 @@ bool two_tiles(int rows, int bk, int bv, int D) {
 }
 
 std::mutex g_tree_mu;
-bool g_tree_set[64][4];   // per device ordinal: shared-memory limits raised
+bool g_tree_set[64][8];   // per device ordinal: shared-memory limits raised
 
 }  // namespace
 
@@ -995,14 +1023,19 @@ cudaError_t launch_tree(const TreeParams &p0, int D, cudaStream_t st) {
     }
     const int smem = std::max(fixed + 4 * (p.dk * pk + p.dv * pv), 120 * 1024);   // one CTA per SM (its 512 TMEM columns)
     using Fn = void (*)(const TreeParams);
-    const Fn fn = D == 128 ? (two ? tree_kernel<128, true> : tree_kernel<128, false>)
-                           : (two ? tree_kernel<64, true> : tree_kernel<64, false>);
+    // copies: as many as the rows leave room for (four: each softmax warp takes 32 of a tile's
+    // 128 columns instead of one warp taking them all)
+    const int rep = two || rows > 64 ? 1 : (rows > 32 ? 2 : 4);
+    const Fn fn = D == 128 ? (two ? tree_kernel<128, true, 1> : rep == 1 ? tree_kernel<128, false, 1>
+                              : rep == 2 ? tree_kernel<128, false, 2> : tree_kernel<128, false, 4>)
+                           : (two ? tree_kernel<64, true, 1> : rep == 1 ? tree_kernel<64, false, 1>
+                              : rep == 2 ? tree_kernel<64, false, 2> : tree_kernel<64, false, 4>);
     {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
         std::lock_guard<std::mutex> lk(g_tree_mu);
-        const int slot = (D == 128 ? 2 : 0) + (two ? 1 : 0);
+        const int slot = (D == 128 ? 4 : 0) + (two ? 3 : rep >> 1);
         if (dev >= 64 || !g_tree_set[dev][slot]) {
             e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
             if (e != cudaSuccess) return e;
