@@ -8,10 +8,10 @@
 // part of one unit's keys against its rows.  Roles:
 //   warps 0-7   softmax: two slots of 128 threads, a thread per row of the slot's score tile.
 //   warps 8-15  unpack: warp 8 + w writes key block w (of 4) of each 128-token tile as fp16
-//               code * scale + zero, warp 12 + w the value block; packed parts come through
-//               the warp's own ring of bulk copies.
-//   warp 16     one thread issues the MMAs: S = Q K^T (operands in shared memory), O += P V
-//               (P in tensor memory over S's first columns).
+//               code * scale + zero, warp 12 + w the value block.
+//   warp 16     issues the MMAs: S = Q K^T (operands in shared memory), O += P V (P in tensor
+//               memory over S's first columns).
+//   warp 17     lane w issues the bulk copies of unpack warp w's packed parts.
 // While one slot is in its softmax the other's MMAs run.
 //
 // Rows and slots.  More than 128 rows (TWO): slot j has row tile j, so each packed block is
@@ -51,7 +51,7 @@ namespace kvq {
 namespace {
 
 constexpr float kLog2eT = 1.4426950408889634f;
-constexpr int kTreeThreads = 17 * 32;
+constexpr int kTreeThreads = 18 * 32;
 constexpr int kTile = 128;              // tokens of a key tile, rows of a row tile
 constexpr float kWeightBias = 7.f;      // weights are 2^(s - m + 7), s - m <= 8
 constexpr float kLag = 8.f;
@@ -79,6 +79,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -140,7 +146,7 @@ struct TreeSmem {
     static constexpr int kscale = rowscale + 256 * 4;
     static constexpr int kpos = kscale + 4 * kTile * 4;
     static constexpr int bars = kpos + 4 * kTile * 4;           // barriers, TMEM address, flags
-    static constexpr int ring = bars + 512;                     // packed parts
+    static constexpr int ring = bars + 768;                     // packed parts
     // the end: (m, l) of the 256 softmax threads over the row scales .. positions, and their O
     // rows (D + 4 floats) over the operand tiles
     static constexpr int ml = rowscale;
@@ -150,11 +156,11 @@ struct TreeSmem {
 
 struct TreeBars {
     uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2];
-    uint64_t part_full[8][4];   // packed parts, per unpack warp and stage
+    uint64_t part_full[8][4], part_free[8][4];   // packed parts, per unpack warp and stage
     uint32_t tmem, bad_value;
     int min_pos;
 };
-static_assert(sizeof(TreeBars) <= 512, "barrier area");
+static_assert(sizeof(TreeBars) <= 768, "barrier area");
 
 // Token of column `col` of a tile, and the column of token u of block w.
 __host__ __device__ constexpr int tile_token(int col) {
@@ -202,106 +208,141 @@ __device__ __forceinline__ uint32_t hfma2_bits(uint32_t c, uint32_t s, uint32_t 
 }
 __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) { return h2_bits(__hmul2(bits_h2(a), bits_h2(b))); }
 
+// W consecutive words (4, 2 or 1) of shared memory.
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
+    if constexpr (W == 4) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+    } else if constexpr (W == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    } else {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+    }
+}
+// Byte offset, within a half's code area, of a lane's words [BITS / 2 * i, ..) : the words of
+// eight consecutive slots (a 32-channel step of keys, a channel group of values).
+template <int BITS, int D>
+__device__ __forceinline__ int step_words(int i, int lane) {
+    constexpr int WH = D * BITS / 64, C = WH < 4 ? WH : 4, W = BITS / 2;   // words of a half, chunk, of a step
+    const int w = W * i;
+    return ((w / C) * 32 * C + lane * C + w % C) * 4;
+}
+
 // Key block w of a tile (part: [codes][s/z] in shared memory) -> fp16 rows of the K operand.
-// pre: an exact power of two (half2) when the layer's values would leave fp16's range, else 0.
-template <int BK, int KM, int D>
+// PRE: scales and zeros times `pre`, an exact power of two (layers whose values would leave
+// fp16's range).  A loop step covers the 32 channels of one 16-byte chunk index; it is not
+// unrolled: four copies of the step's code do not fit the instruction caches beside the other
+// roles'.
+template <int BK, int KM, int D, bool PRE>
 __device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, int w, int lane, uint32_t pre) {
-    constexpr int NJ = D / 32, PK = 16 / BK, WHK = D * BK / 64, KC = 4 * D * BK;
+    constexpr int NJ = D / 32, PK = 16 / BK, KC = 4 * D * BK, W = BK / 2;
     const int g = lane >> 2, t = lane & 3;
-    uint32_t kw[2][WHK];
-    load_lane_words<WHK>(part, lane, kw[0]);
-    load_lane_words<WHK>(part + 2 * D * BK, lane, kw[1]);
+    const uint32_t ps = smem_u32(part);
     // row of token u = 16 kk + 8 i + g, n = 2 kk + i: row0 + 4 kk + 2 i; its 16-byte chunk
     // 2 t + i2 is XOR-ed with the row's low bits (g & 1) + 4 kk + 2 i: all but the lane's own
     // part is constant
     const uint32_t at0 = smem_u32(kt) + tile_col(w, g) * 128 + (((2 * t) ^ (g & 1)) << 4);
+#pragma unroll 1
+    for (int i = 0; i < D / 32; ++i) {   // channels 32 i ..: chunk i2 = i % 2 of sub-tile i / 2
+        const uint32_t at = (at0 ^ ((i & 1) << 4)) + (i >> 1) * (kTile * 128);
+        uint32_t kw[2][W], s[2][2], z[2][2];
+        lds_words<W>(ps + step_words<BK, D>(i, lane), kw[0]);
+        lds_words<W>(ps + 2 * D * BK + step_words<BK, D>(i, lane), kw[1]);
+        if constexpr (KM == 0) {
 #pragma unroll
-    for (int ks = 0; ks < D / 64; ++ks)
-#pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-            uint32_t s[2][2], z[2][2];   // [k][r] (per-channel keys)
-            if constexpr (KM == 0) {
-#pragma unroll
-                for (int k1 = 0; k1 < 2; ++k1) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(part + KC + 16 * (4 * (4 * ks + 2 * i2 + k1) + t));
-                    s[k1][0] = a.x; z[k1][0] = a.y; s[k1][1] = a.z; z[k1][1] = a.w;
-                    if (pre) {
-                        s[k1][0] = hmul2_bits(s[k1][0], pre); z[k1][0] = hmul2_bits(z[k1][0], pre);
-                        s[k1][1] = hmul2_bits(s[k1][1], pre); z[k1][1] = hmul2_bits(z[k1][1], pre);
-                    }
+            for (int k1 = 0; k1 < 2; ++k1) {   // scale and zero pairs of channels 32 i + 16 k1 + 8 r + 2 t, +1
+                uint32_t a[4];
+                lds_words<4>(ps + KC + 16 * (4 * (2 * i + k1) + t), a);
+                s[k1][0] = a[0]; z[k1][0] = a[1]; s[k1][1] = a[2]; z[k1][1] = a[3];
+                if constexpr (PRE) {
+                    s[k1][0] = hmul2_bits(s[k1][0], pre); z[k1][0] = hmul2_bits(z[k1][0], pre);
+                    s[k1][1] = hmul2_bits(s[k1][1], pre); z[k1][1] = hmul2_bits(z[k1][1], pre);
                 }
-            }
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                uint32_t st = 0, zt = 0;
-                if constexpr (KM == 1) {   // scale of (token, 32-channel group 2 ks + i2)
-                    const int u = 8 * n + g;
-                    const uint8_t *a = part + KC + quant::tok_sz_off(u, 2 * ks + i2, NJ);
-                    st = *reinterpret_cast<const uint16_t *>(a) * 0x10001u;
-                    zt = *reinterpret_cast<const uint16_t *>(a + 4 * NJ) * 0x10001u;
-                    if (pre) { st = hmul2_bits(st, pre); zt = hmul2_bits(zt, pre); }
-                }
-                uint32_t o[4];
-#pragma unroll
-                for (int k1 = 0; k1 < 2; ++k1)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int slot = (2 * (4 * ks + 2 * i2 + k1) + (n & 1)) * 2 + r;
-                        const uint32_t c2 = unpack<BK>(kw[n >> 1][slot / PK], slot % PK);
-                        o[2 * k1 + r] = KM == 0 ? hfma2_bits(c2, s[k1][r], z[k1][r]) : hfma2_bits(c2, st, zt);
-                    }
-                const int low = 4 * (n >> 1) + 2 * (n & 1);
-                sts128((at0 ^ ((low ^ i2) << 4)) + ks * (kTile * 128) + low * 128, o[0], o[1], o[2], o[3]);
             }
         }
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            uint32_t st = 0, zt = 0;
+            if constexpr (KM == 1) {   // scale of (token, 32-channel group i)
+                const uint8_t *a = part + KC + quant::tok_sz_off(8 * n + g, i, NJ);
+                st = *reinterpret_cast<const uint16_t *>(a) * 0x10001u;
+                zt = *reinterpret_cast<const uint16_t *>(a + 4 * NJ) * 0x10001u;
+                if constexpr (PRE) { st = hmul2_bits(st, pre); zt = hmul2_bits(zt, pre); }
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int k1 = 0; k1 < 2; ++k1)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int slot = (2 * k1 + (n & 1)) * 2 + r;   // of the step's eight
+                    const uint32_t c2 = unpack<BK>(kw[n >> 1][slot / PK], slot % PK);
+                    o[2 * k1 + r] = KM == 0 ? hfma2_bits(c2, s[k1][r], z[k1][r]) : hfma2_bits(c2, st, zt);
+                }
+            const int low = 4 * (n >> 1) + 2 * (n & 1);
+            sts128((at ^ (low << 4)) + low * 128, o[0], o[1], o[2], o[3]);
+        }
+    }
 }
 
 // Value block w of a tile -> fp16 columns of the V operand ([channel][token]); tokens from
-// `valid` on become zeros.
-template <int BV, int D>
+// `valid` on become zeros.  A loop step covers one 32-channel group.
+template <int BV, int D, bool PRE>
 __device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, int w, int lane, int valid, uint32_t pre) {
-    constexpr int NJ = D / 32, KS = D / 16, PV = 16 / BV, WHV = D * BV / 64, VC = 4 * D * BV;
+    constexpr int NJ = D / 32, PV = 16 / BV, VC = 4 * D * BV, W = BV / 2;
     const int g = lane >> 2, t = lane & 3;
-    uint32_t vw[2][WHV];
-    load_lane_words<WHV>(part, lane, vw[0]);
-    load_lane_words<WHV>(part + 2 * D * BV, lane, vw[1]);
-    uint32_t s[4][NJ], z[4][NJ];   // [2 kk + ch][group], a token pair each
+    const uint32_t ps = smem_u32(part);
+    const uint32_t base = smem_u32(vt) + (w >> 1) * (D * 128) + g * 128 + (((2 * t + (w & 1)) ^ g) << 4);
+#pragma unroll 1
+    for (int j = 0; j < NJ; ++j) {
+        uint32_t vw[2][W], s[4], z[4];
+        lds_words<W>(ps + step_words<BV, D>(j, lane), vw[0]);
+        lds_words<W>(ps + 2 * D * BV + step_words<BV, D>(j, lane), vw[1]);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const int u = 8 * n + 2 * t;
-        const uint8_t *a = part + VC + quant::tok_sz_off(u, 0, NJ);
-        if constexpr (NJ == 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(a), y = *reinterpret_cast<const uint4 *>(a + 16);
-            s[n][0] = x.x; s[n][1] = x.y; s[n][2] = x.z; s[n][3] = x.w;
-            z[n][0] = y.x; z[n][1] = y.y; z[n][2] = y.z; z[n][3] = y.w;
-        } else {
-            const uint4 x = *reinterpret_cast<const uint4 *>(a);
-            s[n][0] = x.x; s[n][1] = x.y;
-            z[n][0] = x.z; z[n][1] = x.w;
+        for (int n = 0; n < 4; ++n) {   // token pair 8 n + 2 t, +1
+            lds_words<1>(ps + VC + quant::tok_sz_off(8 * n + 2 * t, j, NJ), &s[n]);
+            lds_words<1>(ps + VC + quant::tok_sz_off(8 * n + 2 * t, j, NJ) + 4 * NJ, &z[n]);
         }
         if (valid < 32) {   // the unused tokens' scales are not written: they may hold anything
-            const uint32_t m = (u < valid ? 0xFFFFu : 0u) | (u + 1 < valid ? 0xFFFF0000u : 0u);
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) { s[n][j] &= m; z[n][j] &= m; }
-        }
-        if (pre) {
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) { s[n][j] = hmul2_bits(s[n][j], pre); z[n][j] = hmul2_bits(z[n][j], pre); }
-        }
-    }
-    const uint32_t base = smem_u32(vt) + (w >> 1) * (D * 128) + g * 128 + (((2 * t + (w & 1)) ^ g) << 4);
-#pragma unroll
-    for (int m = 0; m < KS; ++m)
-#pragma unroll
-        for (int rh = 0; rh < 2; ++rh) {
-            uint32_t o[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                const int slot = 4 * m + 2 * (n & 1) + rh;
-                o[n] = hfma2_bits(unpack<BV>(vw[n >> 1][slot / PV], slot % PV), s[n][m / 2], z[n][m / 2]);
+                const int u = 8 * n + 2 * t;
+                const uint32_t m = (u < valid ? 0xFFFFu : 0u) | (u + 1 < valid ? 0xFFFF0000u : 0u);
+                s[n] &= m;
+                z[n] &= m;
             }
-            sts128(base + (16 * m + 8 * rh) * 128, o[0], o[1], o[2], o[3]);
         }
+        if constexpr (PRE) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) { s[n] = hmul2_bits(s[n], pre); z[n] = hmul2_bits(z[n], pre); }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int rh = 0; rh < 2; ++rh) {
+                uint32_t o[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int slot = 4 * m + 2 * (n & 1) + rh;
+                    o[n] = hfma2_bits(unpack<BV>(vw[n >> 1][slot / PV], slot % PV), s[n], z[n]);
+                }
+                sts128(base + j * (32 * 128) + (16 * m + 8 * rh) * 128, o[0], o[1], o[2], o[3]);
+            }
+    }
+}
+
+// The unpackers by bit width; layers that need `pre` take a path of their own.
+template <int KM, int D, bool PRE>
+__device__ __forceinline__ void unpack_keys_bits(int bits, const uint8_t *part, uint8_t *kt, int w, int lane, uint32_t pre) {
+    if (bits == 8) unpack_keys<8, KM, D, PRE>(part, kt, w, lane, pre);
+    else if (bits == 4) unpack_keys<4, KM, D, PRE>(part, kt, w, lane, pre);
+    else unpack_keys<2, KM, D, PRE>(part, kt, w, lane, pre);
+}
+template <int D, bool PRE>
+__device__ __forceinline__ void unpack_values_bits(int bits, const uint8_t *part, uint8_t *vt, int w, int lane, int valid,
+                                                   uint32_t pre) {
+    if (bits == 8) unpack_values<8, D, PRE>(part, vt, w, lane, valid, pre);
+    else if (bits == 4) unpack_values<4, D, PRE>(part, vt, w, lane, valid, pre);
+    else unpack_values<2, D, PRE>(part, vt, w, lane, valid, pre);
 }
 
 // Byte offset of channel chunk c8 (8 channels d = 8 c8 ..) of `row` in a K-major operand whose
@@ -382,7 +423,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             mbar_init(&bar->p_full[i], 4);
             mbar_init(&bar->o_full[i], 1);
         }
-        for (int i = 0; i < 32; ++i) mbar_init(&bar->part_full[i >> 2][i & 3], 1);
+        for (int i = 0; i < 32; ++i) {
+            mbar_init(&bar->part_full[i >> 2][i & 3], 1);
+            mbar_init(&bar->part_free[i >> 2][i & 3], 1);
+        }
         bar->bad_value = 0;
         bar->min_pos = 0x7FFFFFFF;
         fence_mbar_init();
@@ -430,35 +474,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     };
     const int ek = pre_exp(0, p.bk), ev = pre_exp(1, p.bv);
 
+    // packed parts of unpack warp 8 + w8: its block of tile tb + i or -1 (the open group has
+    // packed values only), bytes and place in the record, stages, ring
+    auto block_of = [&](int w8, int i) {
+        const int w = w8 & 3, ti = tb + i - n_open;
+        if (ti < 0) return w8 == 4 && pad && tb + i == 0 ? L >> 5 : -1;
+        const int blk = 4 * (tile_first + ti) + w;
+        return blk < nblk ? blk : -1;
+    };
+    const int key_part = 4 * D * p.bk + 4 * D, value_part = 4 * D * p.bv + 4 * D;
+    auto ring_of = [&](int w8) {
+        return SM::ring + (w8 < 4 ? w8 * p.dk * key_part : 4 * p.dk * key_part + (w8 - 4) * p.dv * value_part);
+    };
+
     if (warp >= 8 && warp < 16 && n > 0) {
         // ================================================================ unpack warps
-        const int w = (warp - 8) & 3;
-        const bool is_v = warp >= 12;
+        const int w8 = warp - 8, w = w8 & 3;
+        const bool is_v = w8 >= 4;
         const int bits = is_v ? p.bv : p.bk;
-        const int part_bytes = 4 * D * bits + 4 * D;
-        const int part_off = is_v ? 4 * D * p.bk + 4 * D : 0;
+        const int part_bytes = is_v ? value_part : key_part;
         const int stages = is_v ? p.dv : p.dk;
-        const long long rec_bytes = 4LL * D * (p.bk + p.bv) + 8 * D;
-        uint8_t *ring = smem + SM::ring + (is_v ? 4 * p.dk * (4 * D * p.bk + 4 * D) : 0) + w * stages * part_bytes;
-        uint64_t *part_full = bar->part_full[warp - 8];
-        // packed block of this warp in tile tb + i, or -1: the open group has packed values only
-        auto block_of = [&](int i) {
-            const int ti = tb + i - n_open;
-            if (ti < 0) return is_v && pad && tb + i == 0 && w == 0 ? L >> 5 : -1;
-            const int blk = 4 * (tile_first + ti) + w;
-            return blk < nblk ? blk : -1;
-        };
-        auto issue = [&](int i, int st) {
-            if (i >= n) return;
-            const int blk = block_of(i);
-            if (blk >= 0 && lane == 0) {
-                mbar_expect_tx(&part_full[st], part_bytes);
-                bulk_g2s(ring + st * part_bytes,
-                         p.rec + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk) * rec_bytes + part_off, part_bytes,
-                         &part_full[st]);
-            }
-        };
-        for (int i = 0; i < stages; ++i) issue(i, i);
+        const uint8_t *ring = smem + ring_of(w8);
         {   // query rows, REP copies of them; two (D = 128) or four rows per warp and step
             constexpr int RPW = 32 / NL;
             const float sign = p.scale < 0.f ? -1.f : 1.f;
@@ -484,27 +520,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         }
         const uint32_t pre = (is_v ? ev : ek) ? h2_bits(__float2half2_rn(pow2f(-(is_v ? ev : ek)))) : 0u;
         uint64_t *full = is_v ? bar->v_full : bar->k_full, *free_ = is_v ? bar->v_free : bar->k_free;
-        uint32_t part_phase = 0;   // bit per stage
-        for (int i = 0, st = 0; i < n; ++i, st = st + 1 == stages ? 0 : st + 1) {
+        int st = 0, ph = 0;        // the next part's stage and phase (tiles without a part use none)
+        for (int i = 0; i < n; ++i) {
             uint8_t *tile = smem + (is_v ? SM::v : SM::k) + (i & 1) * SM::OPER;
-            const int blk = block_of(i);
-            if (blk >= 0) {
-                wait(&part_full[st], (part_phase >> st) & 1u);
-                part_phase ^= 1u << st;
-            }
+            const int blk = block_of(w8, i);
+            if (blk >= 0) wait(&bar->part_full[w8][st], ph);
             if (i >= 2) wait(&free_[i & 1], ((i >> 1) - 1) & 1);
             const uint8_t *part = ring + st * part_bytes;
             const bool is_open = tb + i < n_open;
             const int j0 = kTile * (tb + i) + 32 * w - pad;   // open tiles: the block's first drafted token
             if (!is_v && blk >= 0) {
                 if (p.kmode == 0) {
-                    if (bits == 8) unpack_keys<8, 0, D>(part, tile, w, lane, pre);
-                    else if (bits == 4) unpack_keys<4, 0, D>(part, tile, w, lane, pre);
-                    else unpack_keys<2, 0, D>(part, tile, w, lane, pre);
+                    if (pre) unpack_keys_bits<0, D, true>(bits, part, tile, w, lane, pre);
+                    else unpack_keys_bits<0, D, false>(bits, part, tile, w, lane, pre);
                 } else {
-                    if (bits == 8) unpack_keys<8, 1, D>(part, tile, w, lane, pre);
-                    else if (bits == 4) unpack_keys<4, 1, D>(part, tile, w, lane, pre);
-                    else unpack_keys<2, 1, D>(part, tile, w, lane, pre);
+                    if (pre) unpack_keys_bits<1, D, true>(bits, part, tile, w, lane, pre);
+                    else unpack_keys_bits<1, D, false>(bits, part, tile, w, lane, pre);
                 }
             } else if (!is_v && is_open) {
                 // bf16 rows: the open group's, or drafted tokens (rows behind them are masked)
@@ -531,9 +562,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 }
             } else if (is_v && blk >= 0) {
                 const int valid = min(32, L - 32 * blk);
-                if (bits == 8) unpack_values<8, D>(part, tile, w, lane, valid, pre);
-                else if (bits == 4) unpack_values<4, D>(part, tile, w, lane, valid, pre);
-                else unpack_values<2, D>(part, tile, w, lane, valid, pre);
+                if (pre) unpack_values_bits<D, true>(bits, part, tile, w, lane, valid, pre);
+                else unpack_values_bits<D, false>(bits, part, tile, w, lane, valid, pre);
             } else if (is_v && is_open && j0 < nk) {
                 // drafted values: token pairs (u, u + 1) of the block
                 const float fs = pow2f(-ev);
@@ -569,38 +599,70 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[i & 1]);
-            issue(i + stages, st);
+            if (lane == 0) {
+                mbar_arrive(&full[i & 1]);
+                if (blk >= 0) mbar_arrive(&bar->part_free[w8][st]);
+            }
+            if (blk >= 0 && ++st == stages) st = 0, ph ^= 1;
         }
+    } else if (warp == 17) {
+        // ================================================================ packed parts
+        if (lane < 8) {
+            const int stages = lane < 4 ? p.dk : p.dv, bytes = lane < 4 ? key_part : value_part;
+            const long long rec_bytes = key_part + value_part;
+            const uint8_t *src = p.rec + (lane < 4 ? 0 : key_part);
+            uint8_t *ring = smem + ring_of(lane);
+            bool lap = false;      // every stage has been used
+            for (int i = 0, st = 0, ph = 0; i < n; ++i) {
+                const int blk = block_of(lane, i);
+                if (blk < 0) continue;
+                if (lap) wait(&bar->part_free[lane][st], ph ^ 1);
+                mbar_expect_tx(&bar->part_full[lane][st], bytes);
+                bulk_g2s(ring + st * bytes, src + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk) * rec_bytes, bytes,
+                         &bar->part_full[lane][st]);
+                if (++st == stages) st = 0, ph ^= 1, lap = true;
+            }
+        }
+        __syncwarp();
     } else if (warp == 16) {
         // ================================================================ MMA issue
-        if (lane == 0 && n > 0) {
+        // The whole warp runs this code and one elected lane issues: descriptors and addresses stay
+        // in uniform registers (issued from a divergent branch, each MMA costs more instructions
+        // than its 64 tensor cycles: 281 us against 200 us at batch 64, context 4096)
+        if (n > 0) {
             constexpr uint32_t IQK = f16_idesc(128, kTile), IPV = f16_idesc(128, D);
             constexpr int STEP = TWO ? 1 : 2;   // tiles from a slot's tile to its next
             wait(&bar->q_full, 0);
             auto qk = [&](int j, int i) {
-                const uint32_t a = smem_u32(smem + SM::q + (TWO ? j * SM::OPER : 0));
-                const uint32_t k = smem_u32(smem + SM::k + (i & 1) * SM::OPER);
+                const uint64_t a = sw128_desc(smem_u32(smem + SM::q + (TWO ? j * SM::OPER : 0)));
+                const uint64_t k = sw128_desc(smem_u32(smem + SM::k + (i & 1) * SM::OPER));
                 if (!TWO || j == 0) wait(&bar->k_full[i & 1], (i >> 1) & 1);
                 fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const int off = (s >> 2) * (kTile * 128) + (s & 3) * 32;
-                    mma_ss(tmem + j * 128, sw128_desc(a + off), sw128_desc(k + off), IQK, s > 0);
+                    for (int s = 0; s < D / 16; ++s) {   // 16 channels: 32 bytes on, 64 channels: the next sub-tile
+                        const int off = ((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4;
+                        mma_ss(tmem + j * 128, a + off, k + off, IQK, s > 0);
+                    }
+                    mma_commit(&bar->s_full[j]);
+                    if (!TWO || j == 1) mma_commit(&bar->k_free[i & 1]);
                 }
-                mma_commit(&bar->s_full[j]);
-                if (!TWO || j == 1) mma_commit(&bar->k_free[i & 1]);
+                __syncwarp();
             };
-            auto pv = [&](int j, int i, int use) {
-                const uint32_t v = smem_u32(smem + SM::v + (i & 1) * SM::OPER);
+            auto pv = [&](int j, int i, int use, bool last) {
+                const uint64_t v = sw128_desc(smem_u32(smem + SM::v + (i & 1) * SM::OPER));
                 if (!TWO || j == 0) wait(&bar->v_full[i & 1], (i >> 1) & 1);
                 wait(&bar->p_full[j], use & 1);
                 fence_after();
+                if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < kTile / 16; ++s)
-                    mma_ts(tmem + 256 + j * 128, tmem + j * 128 + 8 * s, sw128_desc(v + (s >> 2) * (D * 128) + (s & 3) * 32), IPV,
-                           (use > 0 || s > 0) ? 1u : 0u);
-                if (!TWO || j == 1) mma_commit(&bar->v_free[i & 1]);
+                    for (int s = 0; s < kTile / 16; ++s)
+                        mma_ts(tmem + 256 + j * 128, tmem + j * 128 + 8 * s,
+                               v + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), IPV, (use > 0 || s > 0) ? 1u : 0u);
+                    if (!TWO || j == 1) mma_commit(&bar->v_free[i & 1]);
+                    if (last) mma_commit(&bar->o_full[j]);
+                }
+                __syncwarp();
             };
             // MMAs of one thread run in order: a slot's next scores may overwrite the weights
             // that its previous product reads
@@ -609,9 +671,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             else if (n > 1) qk(1, 1);
             for (int i = 0; i < n; ++i)
                 for (int j = TWO ? 0 : i & 1; j < (TWO ? 2 : (i & 1) + 1); ++j) {
-                    pv(j, i, i / STEP);
+                    pv(j, i, i / STEP, i + STEP >= n);
                     if (i + STEP < n) qk(j, i + STEP);
-                    else mma_commit(&bar->o_full[j]);
                 }
         }
         __syncwarp();
