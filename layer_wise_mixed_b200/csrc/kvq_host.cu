@@ -1566,7 +1566,7 @@ void tree_params(kvq_handle *h, int layer, const kvq_score_opts *o, int T, int n
     const int open = g.kmode == KVQ_PER_CHANNEL ? L % 32 : 0;
     const long long seen = p.window ? std::min<long long>(L, static_cast<long long>(p.window) + 128) : L;
     const long long tiles = (open + nk + 127) / 128 + (seen - open + 127) / 128;
-    const int groups = kvq::tree_row_groups(T * p.G, g.bk, g.bv, h->desc.head_dim);
+    const int groups = kvq::tree_row_groups(T * p.G);
     p.S = h->forced_splits > 0 ? static_cast<int>(std::min<long long>(std::min(h->forced_splits, max_splits), std::max(1LL, tiles)))
                                : kvq::tree_splits(p.B, p.Hkv, groups, tiles, max_splits);
 }

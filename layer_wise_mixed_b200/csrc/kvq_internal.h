@@ -314,7 +314,7 @@ cudaError_t launch_tree_merge(const TreeParams &p, int D, cudaStream_t st);
 // Row groups (CTAs of one split of one unit) of a launch with `rows` query rows per kv head,
 // the most splits a launch may use (what partials are sized for), and the split count for
 // `tiles` 128-token tiles per unit.
-int tree_row_groups(int rows, int bk, int bv, int D);
+int tree_row_groups(int rows);
 int tree_max_splits(int B, int Hkv, int rows);
 int tree_splits(int B, int Hkv, int row_groups, long long tiles, int max_splits);
 cudaError_t launch_read(const ReadParams &p, int D, int bk, int bv, int kmode, cudaStream_t st);

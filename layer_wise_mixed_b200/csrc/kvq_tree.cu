@@ -11,7 +11,8 @@
 //               code * scale + zero, warp 12 + w the value block.
 //   warp 16     issues the MMAs: S = Q K^T (operands in shared memory), O += P V (P in tensor
 //               memory over S's first columns).
-//   warp 17     lane w issues the bulk copies of unpack warp w's packed parts.
+//   warps 17, 18 issue the bulk copies of the packed key and value parts, a tile's four blocks
+//               to a stage.
 // While one slot is in its softmax the other's MMAs run.
 //
 // Rows and slots.  More than 128 rows (TWO): slot j has row tile j, so each packed block is
@@ -51,7 +52,7 @@ namespace kvq {
 namespace {
 
 constexpr float kLog2eT = 1.4426950408889634f;
-constexpr int kTreeThreads = 18 * 32;
+constexpr int kTreeThreads = 19 * 32;
 constexpr int kTile = 128;              // tokens of a key tile, rows of a row tile
 constexpr float kWeightBias = 7.f;      // weights are 2^(s - m + 7), s - m <= 8
 constexpr float kLag = 8.f;
@@ -66,35 +67,60 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 __host__ __device__ constexpr uint32_t f16_idesc(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Issued by the lane whose `on` is set.  The predicate is inside the assembly: the code around
+// it stays convergent, so the compiler keeps descriptors and addresses in uniform registers (in
+// a branch that one lane takes, issuing eight of these took 493 cycles instead of 224, as long
+// as they run).
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t on, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_one(uint32_t on, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void expect_one(uint32_t on, uint64_t *bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+        "r"(bytes), "r"(on)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_one(uint32_t on, uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(on)
         : "memory");
 }
 // One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-__device__ __forceinline__ void mma_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+    return p;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 
 #define KVQ_R8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
 // 32 columns of this warp's 32 lanes, one per register; the registers hold the values after
@@ -138,15 +164,14 @@ template <int D, bool TWO>
 struct TreeSmem {
     static constexpr int OPER = kTile * D * 2;                  // one operand tile
     static constexpr int q = 0;                                 // query row tiles
-    static constexpr int k = q + (TWO ? 2 : 1) * OPER;          // two key tiles
-    static constexpr int v = k + 2 * OPER;                      // two value tiles [D channels][128 tokens]
-    static constexpr int rowscale = v + 2 * OPER;               // score scale of each query row [256]
+    static constexpr int kv = q + (TWO ? 2 : 1) * OPER;         // key tiles, value tiles [D channels][128 tokens]
+    static constexpr int rowscale = kv + (TWO ? 3 : 4) * OPER;  // score scale of each query row [256]
     // open tiles: key row scales and positions, [4][128] each (tile i uses stage i % 4: when its
     // keys are written, tile i - 2's scores are done, so tile i - 4's softmax is)
     static constexpr int kscale = rowscale + 256 * 4;
     static constexpr int kpos = kscale + 4 * kTile * 4;
     static constexpr int bars = kpos + 4 * kTile * 4;           // barriers, TMEM address, flags
-    static constexpr int ring = bars + 768;                     // packed parts
+    static constexpr int ring = bars + 512;                     // packed parts
     // the end: (m, l) of the 256 softmax threads over the row scales .. positions, and their O
     // rows (D + 4 floats) over the operand tiles
     static constexpr int ml = rowscale;
@@ -154,13 +179,27 @@ struct TreeSmem {
     static_assert(256 * ROW * 4 <= rowscale && ml + 256 * 8 <= bars, "the joining areas fit");
 };
 
+// Operand buffer of the key (v = 0) or value (v = 1) tile of tile i, and how often it was used
+// before.  One row tile: two buffers for keys, two for values (keys are scored two tiles
+// ahead).  TWO: three buffers in the order of use, K0 V0 K1 V1 ..
+template <bool TWO>
+__device__ __forceinline__ void operand_buffer(int v, int i, int &buf, int &use) {
+    if constexpr (TWO) {
+        use = (2 * i + v) / 3;
+        buf = 2 * i + v - 3 * use;
+    } else {
+        use = i >> 1;
+        buf = 2 * v + (i & 1);
+    }
+}
+
 struct TreeBars {
-    uint64_t q_full, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2];
-    uint64_t part_full[8][4], part_free[8][4];   // packed parts, per unpack warp and stage
+    uint64_t q_full, full[4], free[4], s_full[2], p_full[2], o_full[2];
+    uint64_t part_full[2][4], part_free[2][4];   // packed parts (keys, values), per stage
     uint32_t tmem, bad_value;
     int min_pos;
 };
-static_assert(sizeof(TreeBars) <= 768, "barrier area");
+static_assert(sizeof(TreeBars) <= 512, "barrier area");
 
 // Token of column `col` of a tile, and the column of token u of block w.
 __host__ __device__ constexpr int tile_token(int col) {
@@ -412,23 +451,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const int *depth = p.depth ? p.depth + static_cast<long long>(b) * p.T : nullptr;
     auto row_t = [&](int r) { return (row0 + r) / p.G; };
 
-    if (tid == 0) {
-        mbar_init(&bar->q_full, 8);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar->k_full[i], 4);
-            mbar_init(&bar->k_free[i], 1);
-            mbar_init(&bar->v_full[i], 4);
-            mbar_init(&bar->v_free[i], 1);
-            mbar_init(&bar->s_full[i], 1);
-            mbar_init(&bar->p_full[i], 4);
-            mbar_init(&bar->o_full[i], 1);
+    if (warp == 17) {   // a barrier per lane: 15 of the operand tiles, 16 of the packed parts
+        if (lane < 15) {   // q_full, full, free, s_full, p_full, o_full
+            mbar_init(&bar->q_full + lane, lane == 0 ? 8 : (lane < 5 || lane == 11 || lane == 12 ? 4 : 1));
+        } else if (lane < 31) {
+            mbar_init(&bar->part_full[0][0] + (lane - 15), lane < 23 ? 1 : 4);
+        } else {
+            bar->bad_value = 0;
+            bar->min_pos = 0x7FFFFFFF;
         }
-        for (int i = 0; i < 32; ++i) {
-            mbar_init(&bar->part_full[i >> 2][i & 3], 1);
-            mbar_init(&bar->part_free[i >> 2][i & 3], 1);
-        }
-        bar->bad_value = 0;
-        bar->min_pos = 0x7FFFFFFF;
         fence_mbar_init();
     }
     if (warp == 16) {
@@ -474,62 +505,77 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     };
     const int ek = pre_exp(0, p.bk), ev = pre_exp(1, p.bv);
 
-    // packed parts of unpack warp 8 + w8: its block of tile tb + i or -1 (the open group has
-    // packed values only), bytes and place in the record, stages, ring
-    auto block_of = [&](int w8, int i) {
-        const int w = w8 & 3, ti = tb + i - n_open;
-        if (ti < 0) return w8 == 4 && pad && tb + i == 0 ? L >> 5 : -1;
-        const int blk = 4 * (tile_first + ti) + w;
-        return blk < nblk ? blk : -1;
-    };
+    // packed parts: first block and number of blocks of tile tb + i (the open group has packed
+    // values only); bytes, ring
     const int key_part = 4 * D * p.bk + 4 * D, value_part = 4 * D * p.bv + 4 * D;
-    auto ring_of = [&](int w8) {
-        return SM::ring + (w8 < 4 ? w8 * p.dk * key_part : 4 * p.dk * key_part + (w8 - 4) * p.dv * value_part);
+    auto blocks_of = [&](bool is_v, int i, int &blk0) {
+        const int ti = tb + i - n_open;
+        if (ti < 0) {
+            blk0 = L >> 5;
+            return is_v && pad && tb + i == 0 ? 1 : 0;
+        }
+        blk0 = 4 * (tile_first + ti);
+        return min(4, nblk - blk0);
     };
+    auto ring_of = [&](bool is_v) { return smem + SM::ring + (is_v ? 4 * p.dk * key_part : 0); };
 
     if (warp >= 8 && warp < 16 && n > 0) {
         // ================================================================ unpack warps
-        const int w8 = warp - 8, w = w8 & 3;
+        const int w8q = warp - 8, w8 = w8q, w = w8 & 3;
         const bool is_v = w8 >= 4;
         const int bits = is_v ? p.bv : p.bk;
         const int part_bytes = is_v ? value_part : key_part;
         const int stages = is_v ? p.dv : p.dk;
-        const uint8_t *ring = smem + ring_of(w8);
-        {   // query rows, REP copies of them; two (D = 128) or four rows per warp and step
-            constexpr int RPW = 32 / NL;
+        const uint8_t *ring = ring_of(is_v) + w * part_bytes;
+        const uint32_t on = elect_one();
+        {   // query rows, REP copies of them; a warp takes RPW rows per step, four steps' loads first
+            constexpr int RPW = 32 / NL, STEPS = ROWS / (8 * RPW), BATCH = STEPS < 4 ? STEPS : 4;
             const float sign = p.scale < 0.f ? -1.f : 1.f;
             const float base = fabsf(p.scale) * kLog2eT * pow2f(ek);
             const int c8 = lane % NL;
-            for (int r0 = (warp - 8) * RPW; r0 < ROWS; r0 += 8 * RPW) {
-                const int r = r0 + lane / NL;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (r < nrow) {
-                    const int t = row_t(r), g = (row0 + r) - t * p.G;
-                    x = *reinterpret_cast<const uint4 *>(p.q + ((static_cast<long long>(b) * p.T + t) * Hq + h * p.G + g) * D +
-                                                         8 * c8);
-                }
-                float inv = 1.f;
+            const uint16_t *q0 = p.q + (static_cast<long long>(b) * p.T * Hq + h * p.G) * D + 8 * c8;
+#pragma unroll 1
+            for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
+                uint4 x[BATCH];
 #pragma unroll
-                for (int k = 0; k < REP; ++k)
-                    inv = store_scaled_row<NL>(smem + SM::q + (r >> 7) * SM::OPER, (r & 127) + k * COPY, c8, x, sign);
-                if (c8 == 0) rowscale[r] = base * inv;
+                for (int k = 0; k < BATCH; ++k) {
+                    const int r = (8 * (s0 + k) + w8q) * RPW + lane / NL;
+                    x[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < nrow) {
+                        const int t = row_t(r), g = (row0 + r) - t * p.G;
+                        x[k] = *reinterpret_cast<const uint4 *>(q0 + (static_cast<long long>(t) * Hq + g) * D);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int r = (8 * (s0 + k) + w8q) * RPW + lane / NL;
+                    float inv = 1.f;
+#pragma unroll
+                    for (int cp = 0; cp < REP; ++cp)
+                        inv = store_scaled_row<NL>(smem + SM::q + (r >> 7) * SM::OPER, (r & 127) + cp * COPY, c8, x[k], sign);
+                    if (c8 == 0) rowscale[r] = base * inv;
+                }
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->q_full);
+            arrive_one(on, &bar->q_full);
         }
         const uint32_t pre = (is_v ? ev : ek) ? h2_bits(__float2half2_rn(pow2f(-(is_v ? ev : ek)))) : 0u;
-        uint64_t *full = is_v ? bar->v_full : bar->k_full, *free_ = is_v ? bar->v_free : bar->k_free;
         int st = 0, ph = 0;        // the next part's stage and phase (tiles without a part use none)
         for (int i = 0; i < n; ++i) {
-            uint8_t *tile = smem + (is_v ? SM::v : SM::k) + (i & 1) * SM::OPER;
-            const int blk = block_of(w8, i);
-            if (blk >= 0) wait(&bar->part_full[w8][st], ph);
-            if (i >= 2) wait(&free_[i & 1], ((i >> 1) - 1) & 1);
-            const uint8_t *part = ring + st * part_bytes;
+            int buf, used;
+            operand_buffer<TWO>(is_v, i, buf, used);
+            uint8_t *tile = smem + SM::kv + buf * SM::OPER;
+            int blk;
+            const int nb = blocks_of(is_v, i, blk);
+            const bool has = w < nb;                          // this warp's block is packed
+            blk += w;
+            if (has) wait(&bar->part_full[is_v][st], ph);
+            if (used > 0) wait(&bar->free[buf], (used - 1) & 1);
+            const uint8_t *part = ring + st * 4 * part_bytes;
             const bool is_open = tb + i < n_open;
             const int j0 = kTile * (tb + i) + 32 * w - pad;   // open tiles: the block's first drafted token
-            if (!is_v && blk >= 0) {
+            if (!is_v && has) {
                 if (p.kmode == 0) {
                     if (pre) unpack_keys_bits<0, D, true>(bits, part, tile, w, lane, pre);
                     else unpack_keys_bits<0, D, false>(bits, part, tile, w, lane, pre);
@@ -541,26 +587,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 // bf16 rows: the open group's, or drafted tokens (rows behind them are masked)
                 float *ksc = reinterpret_cast<float *>(smem + SM::kscale) + (i & 3) * kTile;
                 int *kp = reinterpret_cast<int *>(smem + SM::kpos) + (i & 3) * kTile;
-                constexpr int RPW = 32 / NL;
+                constexpr int RPW = 32 / NL, BATCH = 4;
                 const int c8 = lane % NL;
-                for (int u0 = 0; u0 < 32 && (j0 < 0 || j0 + u0 < nk); u0 += RPW) {
-                    const int u = u0 + lane / NL, row = tile_col(w, u);
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    int pos = 0;
-                    if (j0 < 0) {
-                        if (u < open) x = *reinterpret_cast<const uint4 *>(p.res + (unit * 32 + u) * D + 8 * c8);
-                        pos = (L & ~31) + u;
-                    } else if (j0 + u < nk) {
-                        x = *reinterpret_cast<const uint4 *>(p.kd + (unit * p.T + j0 + u) * D + 8 * c8);
-                        pos = L + (depth ? depth[j0 + u] : j0 + u);
+                const int rows = j0 < 0 ? open : min(32, nk - j0);
+                const uint16_t *k0 = j0 < 0 ? p.res + unit * 32 * D : p.kd + (unit * p.T + j0) * D;
+#pragma unroll 1
+                for (int u0 = 0; u0 < rows; u0 += RPW * BATCH) {
+                    uint4 x[BATCH];
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int u = u0 + k * RPW + lane / NL;
+                        x[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (u < rows) x[k] = *reinterpret_cast<const uint4 *>(k0 + u * D + 8 * c8);
                     }
-                    const float inv = store_scaled_row<NL>(tile, row, c8, x, 1.f);
-                    if (c8 == 0) {
-                        ksc[row] = inv * pow2f(-ek);   // the row scale carries 2^ek for the cached keys
-                        kp[row] = pos;
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int u = u0 + k * RPW + lane / NL, row = tile_col(w, u);
+                        const float inv = store_scaled_row<NL>(tile, row, c8, x[k], 1.f);
+                        if (c8 == 0) ksc[row] = inv * pow2f(-ek);   // the row scale carries 2^ek for the cached keys
                     }
                 }
-            } else if (is_v && blk >= 0) {
+                if (p.alibi || p.window)   // key positions (only these read them)
+                    kp[tile_col(w, lane)] =
+                        j0 < 0 ? (L & ~31) + lane : (lane < rows ? L + (depth ? depth[j0 + lane] : j0 + lane) : 0);
+            } else if (is_v && has) {
                 const int valid = min(32, L - 32 * blk);
                 if (pre) unpack_values_bits<D, true>(bits, part, tile, w, lane, valid, pre);
                 else unpack_values_bits<D, false>(bits, part, tile, w, lane, valid, pre);
@@ -599,70 +649,72 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&full[i & 1]);
-                if (blk >= 0) mbar_arrive(&bar->part_free[w8][st]);
+            arrive_one(on, &bar->full[buf]);
+            if (nb > 0) {
+                arrive_one(on, &bar->part_free[is_v][st]);
+                if (++st == stages) st = 0, ph ^= 1;
             }
-            if (blk >= 0 && ++st == stages) st = 0, ph ^= 1;
         }
-    } else if (warp == 17) {
+    } else if (warp >= 17) {
         // ================================================================ packed parts
-        if (lane < 8) {
-            const int stages = lane < 4 ? p.dk : p.dv, bytes = lane < 4 ? key_part : value_part;
-            const long long rec_bytes = key_part + value_part;
-            const uint8_t *src = p.rec + (lane < 4 ? 0 : key_part);
-            uint8_t *ring = smem + ring_of(lane);
-            bool lap = false;      // every stage has been used
-            for (int i = 0, st = 0, ph = 0; i < n; ++i) {
-                const int blk = block_of(lane, i);
-                if (blk < 0) continue;
-                if (lap) wait(&bar->part_free[lane][st], ph ^ 1);
-                mbar_expect_tx(&bar->part_full[lane][st], bytes);
-                bulk_g2s(ring + st * bytes, src + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk) * rec_bytes, bytes,
-                         &bar->part_full[lane][st]);
-                if (++st == stages) st = 0, ph ^= 1, lap = true;
-            }
+        const bool is_v = warp == 18;
+        const int stages = is_v ? p.dv : p.dk, bytes = is_v ? value_part : key_part;
+        const long long rec_bytes = key_part + value_part;
+        const uint8_t *src = p.rec + (is_v ? key_part : 0);
+        const uint32_t ring = smem_u32(ring_of(is_v)), on = elect_one();
+        bool lap = false;      // every stage has been used
+        for (int i = 0, st = 0, ph = 0; i < n; ++i) {
+            int blk0;
+            const int nb = blocks_of(is_v, i, blk0);
+            if (nb <= 0) continue;
+            if (lap) wait(&bar->part_free[is_v][st], ph ^ 1);
+            __syncwarp();
+            expect_one(on, &bar->part_full[is_v][st], nb * bytes);
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (w < nb)
+                    bulk_one(on, ring + (st * 4 + w) * bytes,
+                             src + rec_index(p.btab, b, p.Hkv, h, p.cap_blk, blk0 + w) * rec_bytes, bytes,
+                             &bar->part_full[is_v][st]);
+            if (++st == stages) st = 0, ph ^= 1, lap = true;
         }
-        __syncwarp();
     } else if (warp == 16) {
         // ================================================================ MMA issue
-        // The whole warp runs this code and one elected lane issues: descriptors and addresses stay
-        // in uniform registers (issued from a divergent branch, each MMA costs more instructions
-        // than its 64 tensor cycles: 281 us against 200 us at batch 64, context 4096)
         if (n > 0) {
+            const uint32_t on = elect_one();
             constexpr uint32_t IQK = f16_idesc(128, kTile), IPV = f16_idesc(128, D);
             constexpr int STEP = TWO ? 1 : 2;   // tiles from a slot's tile to its next
             wait(&bar->q_full, 0);
             auto qk = [&](int j, int i) {
                 const uint64_t a = sw128_desc(smem_u32(smem + SM::q + (TWO ? j * SM::OPER : 0)));
-                const uint64_t k = sw128_desc(smem_u32(smem + SM::k + (i & 1) * SM::OPER));
-                if (!TWO || j == 0) wait(&bar->k_full[i & 1], (i >> 1) & 1);
+                int buf, used;
+                operand_buffer<TWO>(0, i, buf, used);
+                const uint64_t k = sw128_desc(smem_u32(smem + SM::kv + buf * SM::OPER));
+                if (!TWO || j == 0) wait(&bar->full[buf], used & 1);
                 fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {   // 16 channels: 32 bytes on, 64 channels: the next sub-tile
-                        const int off = ((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4;
-                        mma_ss(tmem + j * 128, a + off, k + off, IQK, s > 0);
-                    }
-                    mma_commit(&bar->s_full[j]);
-                    if (!TWO || j == 1) mma_commit(&bar->k_free[i & 1]);
-                }
                 __syncwarp();
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {   // 16 channels: 32 bytes on, 64 channels: the next sub-tile
+                    const int off = ((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4;
+                    mma_ss(on, tmem + j * 128, a + off, k + off, IQK, s > 0);
+                }
+                mma_commit(on, &bar->s_full[j]);
+                if (!TWO || j == 1) mma_commit(on, &bar->free[buf]);
             };
             auto pv = [&](int j, int i, int use, bool last) {
-                const uint64_t v = sw128_desc(smem_u32(smem + SM::v + (i & 1) * SM::OPER));
-                if (!TWO || j == 0) wait(&bar->v_full[i & 1], (i >> 1) & 1);
+                int buf, used;
+                operand_buffer<TWO>(1, i, buf, used);
+                const uint64_t v = sw128_desc(smem_u32(smem + SM::kv + buf * SM::OPER));
+                if (!TWO || j == 0) wait(&bar->full[buf], used & 1);
                 wait(&bar->p_full[j], use & 1);
                 fence_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int s = 0; s < kTile / 16; ++s)
-                        mma_ts(tmem + 256 + j * 128, tmem + j * 128 + 8 * s,
-                               v + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), IPV, (use > 0 || s > 0) ? 1u : 0u);
-                    if (!TWO || j == 1) mma_commit(&bar->v_free[i & 1]);
-                    if (last) mma_commit(&bar->o_full[j]);
-                }
                 __syncwarp();
+#pragma unroll
+                for (int s = 0; s < kTile / 16; ++s)
+                    mma_ts(on, tmem + 256 + j * 128, tmem + j * 128 + 8 * s,
+                           v + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), IPV, (use > 0 || s > 0) ? 1u : 0u);
+                if (!TWO || j == 1) mma_commit(on, &bar->free[buf]);
+                if (last) mma_commit(on, &bar->o_full[j]);
             };
             // MMAs of one thread run in order: a slot's next scores may overwrite the weights
             // that its previous product reads
@@ -678,6 +730,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         __syncwarp();
     } else if (warp < 8) {
         // ================================================================ softmax
+        const uint32_t on = elect_one();
         const int j = warp >> 2;                                 // slot
         const int r = TWO ? tid : (tid & 127) % COPY;            // query row of the CTA
         const int copy = TWO ? 0 : (tid & 127) / COPY;
@@ -875,7 +928,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->p_full[j]);
+            arrive_one(on, &bar->p_full[j]);
         }
         // ---- the end: join slots and copies, write rows
         if (n > 0) wait(&bar->o_full[0], 0);
@@ -1025,27 +1078,20 @@ int fixed_bytes(int D, bool two) {
     if (D == 128) return two ? TreeSmem<128, true>::ring : TreeSmem<128, false>::ring;
     return two ? TreeSmem<64, true>::ring : TreeSmem<64, false>::ring;
 }
-// Two row tiles per CTA need 128 KB of operand tiles more than one stage of every part leaves
-// for 8-bit keys and values at head_dim 128: those run one row tile per CTA.
-bool two_tiles(int rows, int bk, int bv, int D) {
-    return rows > kTile && fixed_bytes(D, true) + 4 * (part_bytes(D, bk) + part_bytes(D, bv)) <= kSmemMax;
-}
+static_assert(TreeSmem<128, true>::ring + 8 * (4 * 128 * 8 + 4 * 128) <= kSmemMax, "one stage of every part fits");
 
 std::mutex g_tree_mu;
 bool g_tree_set[64][8];   // per device ordinal: shared-memory limits raised
 
 }  // namespace
 
-int tree_row_groups(int rows, int bk, int bv, int D) {
-    const int per = two_tiles(rows, bk, bv, D) ? 256 : 128;
-    return (rows + per - 1) / per;
-}
+int tree_row_groups(int rows) { return (rows + 255) / 256; }
 
 constexpr int kTreeSms = 148;
 
 // Partials are sized for at most four CTAs per SM.
 int tree_max_splits(int B, int Hkv, int rows) {
-    const long long ctas = static_cast<long long>(B) * Hkv * ((rows + 255) / 256);
+    const long long ctas = static_cast<long long>(B) * Hkv * tree_row_groups(rows);
     return static_cast<int>(std::max(1LL, std::min(64LL, 4LL * kTreeSms / ctas)));
 }
 
@@ -1067,8 +1113,8 @@ int tree_splits(int B, int Hkv, int row_groups, long long tiles, int max_splits)
 cudaError_t launch_tree(const TreeParams &p0, int D, cudaStream_t st) {
     TreeParams p = p0;
     const int rows = p.T * p.G;
-    const bool two = two_tiles(rows, p.bk, p.bv, D);
-    const int groups = tree_row_groups(rows, p.bk, p.bv, D);
+    const bool two = rows > kTile;
+    const int groups = tree_row_groups(rows);
     // stages of the packed parts: as many as fit, up to four, the fewer-staged kind first
     const int pk = part_bytes(D, p.bk), pv = part_bytes(D, p.bv), fixed = fixed_bytes(D, two);
     p.dk = p.dv = 1;
