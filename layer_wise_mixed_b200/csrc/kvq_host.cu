@@ -1551,6 +1551,7 @@ void tree_params(kvq_handle *h, int layer, const kvq_score_opts *o, int T, int n
     p.Hkv = h->desc.n_kv_heads;
     p.G = h->desc.n_q_heads / h->desc.n_kv_heads;
     p.T = T;
+    p.gmul = p.G > 1 ? static_cast<unsigned>(((1ull << 32) + p.G - 1) / p.G) : 0u;
     p.cap_blk = h->cap_blk;
     p.mask_words = (T + 31) / 32;
     p.cap = o ? o->softcap : 0.f;

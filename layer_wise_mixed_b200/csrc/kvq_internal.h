@@ -243,6 +243,7 @@ struct TreeParams {
     unsigned *status;
     int B, Hkv, G, T, cap_blk, mask_words;
     int S;                      // splits of every request's tiles (even parts)
+    unsigned gmul;              // ceil(2^32 / G) (x / G = mulhi(x, gmul) for x < 2^29), 0 for G = 1
     int pos0;                   // query position - cached length - depth (0; -1: the last cached token)
     int window;                 // 0: none
     float cap, scale;           // cap 0: none; scale of q . k

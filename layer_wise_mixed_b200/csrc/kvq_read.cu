@@ -59,6 +59,11 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadParams 
         }
         __syncwarp();
     };
+    uint32_t vw[2][WHV];   // loaded up front: on their way while the keys are done
+    if (p.V) {
+        load_lane_words<WHV>(rec + KC + KSZ, lane, vw[0]);
+        load_lane_words<WHV>(rec + KC + KSZ + 2 * D * BV, lane, vw[1]);
+    }
     if (p.K) {
         if (KM == 0 && blk == (L >> 5)) {   // the open group: bf16 rows as they are
             const uint16_t *res = p.res + unit * 32 * D;
@@ -113,9 +118,6 @@ __global__ void __launch_bounds__(kReadWarps * 32) read_kernel(const ReadParams 
         }
     }
     if (p.V) {
-        uint32_t vw[2][WHV];
-        load_lane_words<WHV>(rec + KC + KSZ, lane, vw[0]);
-        load_lane_words<WHV>(rec + KC + KSZ + 2 * D * BV, lane, vw[1]);
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll

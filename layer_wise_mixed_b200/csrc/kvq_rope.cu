@@ -21,7 +21,7 @@
 namespace kvq {
 namespace {
 
-constexpr int kRopeThreads = 384;
+constexpr int kRopeThreads = 384;   // the most threads of a CTA
 
 __device__ __forceinline__ void bf16x8_to_f32(const uint4 &v, float *x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -41,57 +41,59 @@ __device__ __forceinline__ uint4 f32x8_to_bf16(const float *x) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// tpc tokens per CTA; dynamic shared memory: tpc * rot / 2 (cos, sin) pairs
+// A CTA takes tpc tokens: one, or several where a token's rows are few (a persistent grid that
+// fetched the next token while it wrote this one needed 78 registers and took 140 us where
+// this takes KROPE us, 16,384 tokens of 48 rows: threads in flight count for more).  Dynamic shared
+// memory: tpc * rot / 2 (cos, sin) pairs.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int tpc) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams p, int tpc) {
     pdl_enter();
-    extern __shared__ float2 cs[];
+    extern __shared__ float2 cs_s[];
     constexpr int TPR = D / 16;                    // threads per row
     const int rows = p.Hq + 2 * p.Hkv;             // rows of a token
     const int half = p.rot >> 1, rc = p.rot >> 4;  // pairs; threads with rotated chunks
-    const long long tok0 = static_cast<long long>(blockIdx.x) * tpc;
-    const long long tokens = static_cast<long long>(p.B) * p.n;
-    const int nt = static_cast<int>(min(static_cast<long long>(tpc), tokens - tok0));
+    const unsigned tokens = static_cast<unsigned>(p.B) * p.n;   // below 2^31
     const int u = threadIdx.x % TPR;
     const int c0 = u < rc ? u : 2 * u, c1 = u < rc ? u + rc : 2 * u + 1;
-    const int step = blockDim.x / TPR;
     // blockDim is a multiple of 32 and TPR divides 32: a row's threads share a warp, and all
     // lanes of a warp run the same number of passes (inactive rows are clamped, not skipped)
-    const int items = nt * rows, passes = (items + step - 1) / step;
-    uint4 v0, v1;
-    auto src = [&](int it, int &j, int &row, long long &tok) {
-        j = it / rows;
+    const int step = blockDim.x / TPR, first = threadIdx.x / TPR;
+    auto tokens_of = [&](unsigned g) { return min(static_cast<unsigned>(tpc), tokens - g * tpc); };
+    // row `it` of group g: its token (request b, index ti) and row
+    auto place = [&](unsigned g, int it, unsigned &b, unsigned &ti, int &j, int &row) {
+        const int last = static_cast<int>(tokens_of(g)) * rows - 1;
+        it = min(it, last);
+        j = tpc == 1 ? 0 : it / rows;
         row = it - j * rows;
-        tok = tok0 + j;
-        return p.qkv + (tok / p.n) * p.batch_stride + (tok % p.n) * p.token_stride + static_cast<long long>(row) * D;
+        const unsigned tok = g * tpc + j;
+        b = tok / p.n;
+        ti = tok - b * p.n;
     };
-    int j, row;
-    long long tok;
-    {
-        const uint16_t *s = src(min(static_cast<int>(threadIdx.x) / TPR, items - 1), j, row, tok);
+    auto fetch = [&](unsigned g, int it, uint4 &v0, uint4 &v1) {
+        unsigned b, ti;
+        int j, row;
+        place(g, it, b, ti, j, row);
+        const uint16_t *s = p.qkv + b * p.batch_stride + ti * p.token_stride + static_cast<long long>(row) * D;
         v0 = *reinterpret_cast<const uint4 *>(s + 8 * c0);
         v1 = *reinterpret_cast<const uint4 *>(s + 8 * c1);
-    }
-    for (int k = threadIdx.x; k < nt * half; k += blockDim.x) {
-        const int jj = k / half, i = k - jj * half;
-        const long long t = tok0 + jj;
-        const int b = static_cast<int>(t / p.n), ti = static_cast<int>(t % p.n);
-        const double pos = static_cast<double>(p.len.len(b)) + (p.offset ? p.offset[t] : ti);
-        // turns = position * inv_freq / (2 pi): the fraction survives in fp64
-        const double turns = pos * static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;
-        float sn, cn;
-        sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cn);
-        cs[k] = make_float2(cn, sn);
-    }
-    __syncthreads();
-    for (int pass = 0; pass < passes; ++pass) {
-        const int it = pass * step + threadIdx.x / TPR;
-        if (pass) {
-            const uint16_t *s = src(min(it, items - 1), j, row, tok);
-            v0 = *reinterpret_cast<const uint4 *>(s + 8 * c0);
-            v1 = *reinterpret_cast<const uint4 *>(s + 8 * c1);
+    };
+    auto angles = [&](unsigned g, float2 *cs) {
+        const int cnt = static_cast<int>(tokens_of(g)) * half;
+        for (int k = threadIdx.x; k < cnt; k += blockDim.x) {
+            const int j = k / half, i = k - j * half;
+            const unsigned tok = g * tpc + j, b = tok / p.n, ti = tok - b * p.n;
+            const double pos = static_cast<double>(p.len.len(b)) + (p.offset ? p.offset[tok] : static_cast<int>(ti));
+            // turns = position * inv_freq / (2 pi): the fraction survives in fp64
+            const double turns = pos * static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;
+            float sn, cn;
+            sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cn);
+            cs[k] = make_float2(cn, sn);
         }
-        const int b = static_cast<int>(tok / p.n), ti = static_cast<int>(tok % p.n);
+    };
+    auto turn = [&](unsigned g, int it, uint4 v0, uint4 v1, const float2 *cs) {
+        unsigned b, ti;
+        int j, row;
+        place(g, it, b, ti, j, row);
         const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
         const float *w = is_q ? p.wq : p.wk;
         float x[16];
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
 #pragma unroll
         for (int o = 1; o < TPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         uint16_t *dst;
-        if (is_q) dst = p.q + (tok * p.Hq + row) * D;
+        if (is_q) dst = p.q + ((static_cast<long long>(b) * p.n + ti) * p.Hq + row) * D;
         else {
             const int h = row - p.Hq - (is_v ? p.Hkv : 0);
             dst = (is_v ? p.V : p.K) + ((static_cast<long long>(b) * p.Hkv + h) * p.n + ti) * D;
@@ -140,10 +142,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
             v0 = f32x8_to_bf16(x);
             v1 = f32x8_to_bf16(x + 8);
         }
-        if (it < items) {
+        if (it < static_cast<int>(tokens_of(g)) * rows) {
             *reinterpret_cast<uint4 *>(dst + 8 * c0) = v0;
             *reinterpret_cast<uint4 *>(dst + 8 * c1) = v1;
         }
+    };
+    const unsigned g = blockIdx.x;
+    uint4 v0, v1;
+    fetch(g, first, v0, v1);
+    angles(g, cs_s);
+    __syncthreads();
+    const int items = static_cast<int>(tokens_of(g)) * rows;
+    for (int it0 = 0; it0 < items; it0 += step) {   // (uniform over the CTA)
+        uint4 n0 = v0, n1 = v1;
+        if (it0 + step < items) fetch(g, it0 + step + first, n0, n1);   // on its way meanwhile
+        turn(g, it0 + first, v0, v1, cs_s);
+        v0 = n0;
+        v1 = n1;
     }
 }
 
@@ -152,13 +167,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
 cudaError_t launch_rope(const RopeParams &p, cudaStream_t st) {
     const int rows = p.Hq + 2 * p.Hkv, tpr = p.D / 16;
     const long long tokens = static_cast<long long>(p.B) * p.n;
-    // one pass per CTA where a token's rows fill it, several tokens per CTA where they do not
     int tpc = kRopeThreads / (rows * tpr);
     if (tpc < 1) tpc = 1;
     if (tpc > 16) tpc = 16;
-    const int want = (static_cast<int>(tokens < tpc ? tokens : tpc) * rows * tpr + 31) / 32 * 32;
+    if (tokens >= 16 * 1024) tpc = tpc < 8 ? 8 : tpc;   // long prompts: fewer barriers and angle steps per token
+    if (tokens < tpc) tpc = static_cast<int>(tokens);
+    const int want = (tpc * rows * tpr + 31) / 32 * 32;
     const int threads = want < kRopeThreads ? want : kRopeThreads;
-    const long long grid = (tokens + tpc - 1) / tpc;
+    const unsigned grid = static_cast<unsigned>((tokens + tpc - 1) / tpc);
     const size_t smem = static_cast<size_t>(tpc) * (p.rot / 2) * sizeof(float2);   // at most 8 KB
     cudaError_t e = p.D == 128 ? launch_pdl(rope_kernel<128>, dim3(grid), dim3(threads), smem, st, p, tpc)
                                : launch_pdl(rope_kernel<64>, dim3(grid), dim3(threads), smem, st, p, tpc);

@@ -10,7 +10,7 @@
 //   warps 8-15  unpack: warp 8 + w writes key block w (of 4) of each 128-token tile as fp16
 //               code * scale + zero, warp 12 + w the value block.
 //   warp 16     issues the MMAs: S = Q K^T (operands in shared memory), O += P V (P in tensor
-//               memory over S's first columns).
+//               memory over S's last 64 columns).
 //   warps 17, 18 issue the bulk copies of the packed key and value parts, a tile's four blocks
 //               to a stage.
 // While one slot is in its softmax the other's MMAs run.
@@ -52,11 +52,16 @@ namespace kvq {
 namespace {
 
 constexpr float kLog2eT = 1.4426950408889634f;
-constexpr int kTreeThreads = 19 * 32;
+constexpr int kTreeThreads = 20 * 32;    // five warpgroups: register counts are set per warpgroup
+// Registers of a thread: 96 at launch (20 warps); the softmax warps hold a whole score row.
+// 256 x 144 + 256 x 72 + 128 x 40 = 60,416 of the 640 x 96 = 61,440 launched with.
+constexpr int kRegsSoftmax = 144, kRegsUnpack = 72, kRegsIssue = 40;
+static_assert(256 * kRegsSoftmax + 256 * kRegsUnpack + 128 * kRegsIssue <= kTreeThreads * 96, "register split");
 constexpr int kTile = 128;              // tokens of a key tile, rows of a row tile
 constexpr float kWeightBias = 7.f;      // weights are 2^(s - m + 7), s - m <= 8
 constexpr float kLag = 8.f;
 constexpr uint32_t kTmemCols = 512;     // S0, S1, O0, O1
+constexpr int kWeightCol = 64;          // a slot's weights: the last 64 of its 128 score columns
 
 // ------------------------------------------------------------------ tcgen05
 // Shared-memory descriptor: K-major, 128-byte swizzle, 8-row groups 1024 bytes apart.
@@ -138,6 +143,17 @@ __device__ __forceinline__ void ld32_issue(uint32_t taddr, uint32_t *r) {
 }
 __device__ __forceinline__ void ld32_wait(uint32_t *r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : KVQ_R8(r, 0), KVQ_R8(r, 8), KVQ_R8(r, 16), KVQ_R8(r, 24)::"memory");
+}
+__device__ __forceinline__ void ld16_issue(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void ld16_wait(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : KVQ_R8(r, 0), KVQ_R8(r, 8)::"memory");
 }
 __device__ __forceinline__ void st32(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -419,10 +435,26 @@ __device__ __forceinline__ float store_scaled_row(uint8_t *tile, int row, int c8
     return pow2f(e - 14);
 }
 
+// Bounded waits; after one expiry no wait waits again.  The clock is read only after many
+// polls: reading the global timer takes longer than most of these waits.
 struct Waiter {
     bool failed = false;
     __device__ __forceinline__ void operator()(uint64_t *bar, unsigned parity) {
-        if (!failed && !mbar_wait(bar, parity)) failed = true;   // after one expiry no wait waits again
+        if (mbar_try_wait(bar, parity)) return;
+        slow(bar, parity);
+    }
+    __device__ __forceinline__ void slow(uint64_t *bar, unsigned parity) {
+        if (failed) return;
+        uint64_t t0 = 0;
+        for (;;) {
+#pragma unroll 1
+            for (int k = 0; k < 256; ++k)
+                if (mbar_try_wait(bar, parity)) return;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > kWaitLimitNs) break;
+        }
+        failed = true;
     }
 };
 
@@ -448,8 +480,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     if (nrow <= 0) return;
     const int Hq = p.Hkv * p.G;
     const long long unit = static_cast<long long>(b) * p.Hkv + h;
+    const unsigned smax_k = p.smax[0], smax_v = p.smax[1];
     const int *depth = p.depth ? p.depth + static_cast<long long>(b) * p.T : nullptr;
-    auto row_t = [&](int r) { return (row0 + r) / p.G; };
+    auto row_t = [&](int r) { return p.gmul ? static_cast<int>(__umulhi(row0 + r, p.gmul)) : row0 + r; };   // / G
 
     if (warp == 17) {   // a barrier per lane: 15 of the operand tiles, 16 of the packed parts
         if (lane < 15) {   // q_full, full, free, s_full, p_full, o_full
@@ -491,19 +524,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const int n_main = max(0, (nblk + 3) / 4 - tile_first);
     // this split's even part of the tiles: [tb, te), open tiles first
     const int n_all = n_open + n_main;
-    const int tb = static_cast<int>(static_cast<long long>(n_all) * sp / p.S);
-    const int te = static_cast<int>(static_cast<long long>(n_all) * (sp + 1) / p.S);
+    // (at most 2^23 tiles and 64 splits: 32 bits)
+    const int tb = static_cast<unsigned>(n_all) * sp / static_cast<unsigned>(p.S);
+    const int te = static_cast<unsigned>(n_all) * (sp + 1) / static_cast<unsigned>(p.S);
     const int n = te - tb;
     Waiter wait;
 
     // exact power of two that keeps the layer's cached values inside fp16 (1 for any layer whose
     // scales are below 2^14 / (2^b - 1))
-    auto pre_exp = [&](int which, int bits) {
-        const float sm = __half2float(__ushort_as_half(static_cast<unsigned short>(p.smax[which])));
+    auto pre_exp = [&](unsigned smax, int bits) {
+        const float sm = __half2float(__ushort_as_half(static_cast<unsigned short>(smax)));
         const float top = sm * static_cast<float>((1 << bits) - 1);
         return top >= 16384.f ? min(14, floor_log2(top) - 13) : 0;
     };
-    const int ek = pre_exp(0, p.bk), ev = pre_exp(1, p.bv);
+    const int ek = pre_exp(smax_k, p.bk), ev = pre_exp(smax_v, p.bv);
 
     // packed parts: first block and number of blocks of tile tb + i (the open group has packed
     // values only); bytes, ring
@@ -519,47 +553,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     };
     auto ring_of = [&](bool is_v) { return smem + SM::ring + (is_v ? 4 * p.dk * key_part : 0); };
 
-    if (warp >= 8 && warp < 16 && n > 0) {
+    if (warp >= 8 && warp < 16) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUnpack));
+      if (n > 0) {
         // ================================================================ unpack warps
-        const int w8q = warp - 8, w8 = w8q, w = w8 & 3;
+        const int w8 = warp - 8, w = w8 & 3;
         const bool is_v = w8 >= 4;
         const int bits = is_v ? p.bv : p.bk;
         const int part_bytes = is_v ? value_part : key_part;
         const int stages = is_v ? p.dv : p.dk;
         const uint8_t *ring = ring_of(is_v) + w * part_bytes;
         const uint32_t on = elect_one();
-        {   // query rows, REP copies of them; a warp takes RPW rows per step, four steps' loads first
-            constexpr int RPW = 32 / NL, STEPS = ROWS / (8 * RPW), BATCH = STEPS < 4 ? STEPS : 4;
-            const float sign = p.scale < 0.f ? -1.f : 1.f;
-            const float base = fabsf(p.scale) * kLog2eT * pow2f(ek);
-            const int c8 = lane % NL;
-            const uint16_t *q0 = p.q + (static_cast<long long>(b) * p.T * Hq + h * p.G) * D + 8 * c8;
-#pragma unroll 1
-            for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
-                uint4 x[BATCH];
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int r = (8 * (s0 + k) + w8q) * RPW + lane / NL;
-                    x[k] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < nrow) {
-                        const int t = row_t(r), g = (row0 + r) - t * p.G;
-                        x[k] = *reinterpret_cast<const uint4 *>(q0 + (static_cast<long long>(t) * Hq + g) * D);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int r = (8 * (s0 + k) + w8q) * RPW + lane / NL;
-                    float inv = 1.f;
-#pragma unroll
-                    for (int cp = 0; cp < REP; ++cp)
-                        inv = store_scaled_row<NL>(smem + SM::q + (r >> 7) * SM::OPER, (r & 127) + cp * COPY, c8, x[k], sign);
-                    if (c8 == 0) rowscale[r] = base * inv;
-                }
-            }
-            fence_proxy_async();
-            __syncwarp();
-            arrive_one(on, &bar->q_full);
-        }
         const uint32_t pre = (is_v ? ev : ek) ? h2_bits(__float2half2_rn(pow2f(-(is_v ? ev : ek)))) : 0u;
         int st = 0, ph = 0;        // the next part's stage and phase (tiles without a part use none)
         for (int i = 0; i < n; ++i) {
@@ -570,7 +574,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             const int nb = blocks_of(is_v, i, blk);
             const bool has = w < nb;                          // this warp's block is packed
             blk += w;
-            if (has) wait(&bar->part_full[is_v][st], ph);
+            // a warp without a block waits too: its next wait must not meet this phase unfinished
+            if (nb > 0) wait(&bar->part_full[is_v][st], ph);
             if (used > 0) wait(&bar->free[buf], (used - 1) & 1);
             const uint8_t *part = ring + st * 4 * part_bytes;
             const bool is_open = tb + i < n_open;
@@ -655,7 +660,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 if (++st == stages) st = 0, ph ^= 1;
             }
         }
-    } else if (warp >= 17) {
+      }
+    } else if (warp >= 16) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+      if (warp == 17 || warp == 18) {
         // ================================================================ packed parts
         const bool is_v = warp == 18;
         const int stages = is_v ? p.dv : p.dk, bytes = is_v ? value_part : key_part;
@@ -678,9 +686,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                              &bar->part_full[is_v][st]);
             if (++st == stages) st = 0, ph ^= 1, lap = true;
         }
-    } else if (warp == 16) {
+      } else if (warp == 16 && n > 0) {
         // ================================================================ MMA issue
-        if (n > 0) {
+        {
             const uint32_t on = elect_one();
             constexpr uint32_t IQK = f16_idesc(128, kTile), IPV = f16_idesc(128, D);
             constexpr int STEP = TWO ? 1 : 2;   // tiles from a slot's tile to its next
@@ -711,7 +719,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 __syncwarp();
 #pragma unroll
                 for (int s = 0; s < kTile / 16; ++s)
-                    mma_ts(on, tmem + 256 + j * 128, tmem + j * 128 + 8 * s,
+                    mma_ts(on, tmem + 256 + j * 128, tmem + j * 128 + kWeightCol + 8 * s,
                            v + (((s >> 2) * (D * 128) + (s & 3) * 32) >> 4), IPV, (use > 0 || s > 0) ? 1u : 0u);
                 if (!TWO || j == 1) mma_commit(on, &bar->free[buf]);
                 if (last) mma_commit(on, &bar->o_full[j]);
@@ -728,7 +736,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 }
         }
         __syncwarp();
-    } else if (warp < 8) {
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         // ================================================================ softmax
         const uint32_t on = elect_one();
         const int j = warp >> 2;                                 // slot
@@ -742,6 +752,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const int pos = query_pos(rc);
         const float slope2 = p.alibi ? p.alibi[hq] * kLog2eT : 0.f;
         const uint32_t *mrow = p.mask ? p.mask + (static_cast<long long>(b) * p.T + t) * p.mask_words : nullptr;
+        if (n > 0) {   // query rows, REP copies of them; a warp takes RPW rows per step, four steps' loads first
+            constexpr int RPW = 32 / NL, STEPS = ROWS / (8 * RPW), BATCH = STEPS < 4 ? STEPS : 4;
+            const float sign = p.scale < 0.f ? -1.f : 1.f;
+            const float base = fabsf(p.scale) * kLog2eT * pow2f(ek);
+            const int c8 = lane % NL;
+            const uint16_t *q0 = p.q + (static_cast<long long>(b) * p.T * Hq + h * p.G) * D + 8 * c8;
+#pragma unroll 1
+            for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
+                uint4 x[BATCH];
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int r = (8 * (s0 + k) + warp) * RPW + lane / NL;
+                    x[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < nrow) {
+                        const int t = row_t(r), g = (row0 + r) - t * p.G;
+                        x[k] = *reinterpret_cast<const uint4 *>(q0 + (static_cast<long long>(t) * Hq + g) * D);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int r = (8 * (s0 + k) + warp) * RPW + lane / NL;
+                    float inv = 1.f;
+#pragma unroll
+                    for (int cp = 0; cp < REP; ++cp)
+                        inv = store_scaled_row<NL>(smem + SM::q + (r >> 7) * SM::OPER, (r & 127) + cp * COPY, c8, x[k], sign);
+                    if (c8 == 0) rowscale[r] = base * inv;
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            arrive_one(on, &bar->q_full);
+        }
         float m = -INFINITY, l = 0.f, rs = 0.f;
         const int first = TWO ? 0 : j, step = TWO ? 1 : 2;
         int use = 0;
@@ -845,29 +887,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     }
                     return fmaxf(a, d);
                 };
-                // ---- pass 1: row maximum (shaped scores are written back)
-                uint32_t x[32];
-                float mx = -INFINITY;
-                if (NC == 1) {
-                    ld32_issue(ts + 32 * copy, x);
-                    ld32_wait(x);
-                    if (shaped) shape(x, copy);
-                    mx = top(x, mx);
-                } else {
+                const int c0 = copy * NC;                 // the row's chunks [c0, c0 + NC)
+                uint32_t x[NC][32];
+                if (NC > 1 && shaped) {   // shaped scores are written back, then read like plain ones
 #pragma unroll 1
-                    for (int c = copy * NC; c < copy * NC + NC; ++c) {
-                        ld32_issue(ts + 32 * c, x);
-                        ld32_wait(x);
-                        if (shaped) {
-                            shape(x, c);
-                            st32(ts + 32 * c, x);
-                        }
-                        mx = top(x, mx);
+                    for (int c = c0; c < c0 + NC; ++c) {
+                        ld32_issue(ts + 32 * c, x[0]);
+                        ld32_wait(x[0]);
+                        shape(x[0], c);
+                        st32(ts + 32 * c, x[0]);
                     }
-                    if (shaped) st_wait();
+                    st_wait();
                 }
+                // ---- the row's maximum; its last two chunks stay in registers
+                float mx = -INFINITY;
+                if (NC == 4) {
+                    ld32_issue(ts, x[0]);
+                    ld32_issue(ts + 32, x[1]);
+                    ld32_wait(x[0]);
+                    ld32_wait(x[1]);
+                    mx = top(x[1], top(x[0], mx));
+                }
+                constexpr int H = NC > 2 ? 2 : 0;         // first chunk that stays
+#pragma unroll
+                for (int c = H; c < NC; ++c) ld32_issue(ts + 32 * (c0 + c), x[c]);
+#pragma unroll
+                for (int c = H; c < NC; ++c) ld32_wait(x[c]);
+                if (NC == 1 && shaped) shape(x[0], c0);
+#pragma unroll
+                for (int c = H; c < NC; ++c) mx = top(x[c], mx);
                 const float f = shaped ? 1.f : rs;
-                // the maximum moves only when it grew by more than the lag, then O and l are rescaled
+                // the maximum (in log2 units) moves only when it grew by more than the lag, then O and l
+                // are rescaled
                 mx *= f;
                 if (__any_sync(0xffffffffu, mx > m + kLag)) {
                     const float mn = fmaxf(m, mx);
@@ -875,43 +926,44 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         const float al = m == -INFINITY ? 0.f : fast_exp2(m - mn);
                         l *= al;
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t y[32];
-                            ld32_issue(to + 32 * c, y);
-                            ld32_wait(y);
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t y[16];
+                            ld16_issue(to + 16 * c, y);
+                            ld16_wait(y);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * al);
-                            st32(to + 32 * c, y);
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * al);
+                            st16(to + 16 * c, y);
                         }
                     }
                     m = mn;
                 }
-                // ---- pass 2: weights 2^(s - m + bias), their sum, fp16 into tensor memory
+                // ---- weights 2^(s - m + bias), their sum, fp16 into tensor memory over the scores
                 const float sub = m == -INFINITY ? 0.f : kWeightBias - m;
                 const uint64_t f2 = pack2(f, f), sub2 = pack2(sub, sub);
                 uint64_t sum = pack2(0.f, 0.f);
-                auto weigh = [&](const uint32_t *x, int c) {
+                auto weigh = [&](const uint32_t *y, int c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
+                        const uint64_t v = fma2(pack2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])), f2, sub2);
                         float a, d;
-                        unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), f2, sub2), a, d);
+                        unpack2(v, a, d);
                         a = fast_exp2(a);
                         d = fast_exp2(d);
                         sum = add2(sum, pack2(a, d));
                         pk[e] = pack_h2(a, d);
                     }
-                    st16(ts + 16 * c, pk);
+                    st16(ts + kWeightCol + 16 * c, pk);
                 };
-                if (NC == 1) {
-                    weigh(x, copy);
-                } else {
-#pragma unroll 1
-                    for (int c = copy * NC; c < copy * NC + NC; ++c) {
-                        ld32_issue(ts + 32 * c, x);
-                        ld32_wait(x);
-                        weigh(x, c);
-                    }
+                weigh(x[H], c0 + H);
+                if (NC == 4) ld32_issue(ts, x[0]);
+                if (NC > 1) weigh(x[H + 1], c0 + H + 1);
+                if (NC == 4) {
+                    ld32_wait(x[0]);
+                    ld32_issue(ts + 32, x[1]);
+                    weigh(x[0], 0);
+                    ld32_wait(x[1]);
+                    weigh(x[1], 1);
                 }
                 if (REP > 1) {   // the other copies' columns
                     uint32_t zero[16];
@@ -919,7 +971,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     for (int e = 0; e < 16; ++e) zero[e] = 0u;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (c / NC != copy) st16(ts + 16 * c, zero);
+                        if (c / NC != copy) st16(ts + kWeightCol + 16 * c, zero);
                 }
                 float s0, s1;
                 unpack2(sum, s0, s1);

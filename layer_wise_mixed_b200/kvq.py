@@ -7,6 +7,8 @@ CUDA stream, and (in ``Cache``) to allocate the caller-owned workspace.
 """
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
 import os
 import re
@@ -128,10 +130,17 @@ def _check(rc: int):
     return rc
 
 
+_raw_stream = None   # torch's raw-handle form of current_stream (no Stream object per call)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _raw_stream = (lambda: get(dev())) if get else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -325,17 +334,27 @@ def _opt_ptr(x):
 
 
 def _host_i32(x):
-    """(pointer, array kept alive) of an optional host int32 array."""
+    """(address, array kept alive) of an optional host int32 array."""
     if x is None:
         return None, None
-    a = np.ascontiguousarray(x, np.int32)
-    return a.ctypes.data_as(ctypes.c_void_p), a
+    a = array.array("i", x) if isinstance(x, (list, tuple)) else np.ascontiguousarray(x, np.int32)
+    return (a.buffer_info()[0] if isinstance(a, array.array) else a.ctypes.data), a
+
+
+def _ref(s):
+    """byref of an optional structure (Rope and ScoreOpts hold theirs)."""
+    if s is None:
+        return None
+    return getattr(s, "ref", None) or ctypes.byref(s)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def kvq_norm_rope(h: int, layer: int, qkv, batch_stride: int, token_stride: int, n: int, offset, rope: kvq_rope_desc,
                   q, K, V, stream=None):
     _check(load().kvq_norm_rope(h, layer, _ptr(qkv), batch_stride, token_stride, n, _opt_ptr(offset),
-                                ctypes.byref(rope), _ptr(q), _ptr(K), _ptr(V), _stream(stream)))
+                                _ref(rope), _ptr(q), _ptr(K), _ptr(V), _stream(stream)))
 
 
 def kvq_tree_attn_workspace_bytes(h: int, T: int) -> int:
@@ -348,12 +367,11 @@ def kvq_tree_attn(h: int, layer: int, q, K, V, T: int, n_draft, mask, depth, opt
                   out_fp32: bool, workspace, workspace_bytes: int, stream=None):
     nd, keep = _host_i32(n_draft)
     _check(load().kvq_tree_attn(h, layer, _ptr(q), _ptr(K), _ptr(V), T, nd, _opt_ptr(mask), _opt_ptr(depth),
-                                None if opts is None else ctypes.byref(opts), _ptr(out), int(bool(out_fp32)),
-                                _ptr(workspace), workspace_bytes, _stream(stream)))
+                                _ref(opts), _ptr(out), int(bool(out_fp32)), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def kvq_decode_attn_scored(h: int, layer: int, q, opts: Optional[kvq_score_opts], out, out_fp32: bool, stream=None):
-    _check(load().kvq_decode_attn_scored(h, layer, _ptr(q), None if opts is None else ctypes.byref(opts), _ptr(out),
+    _check(load().kvq_decode_attn_scored(h, layer, _ptr(q), _ref(opts), _ptr(out),
                                          int(bool(out_fp32)), _stream(stream)))
 
 
@@ -379,6 +397,11 @@ class Rope(kvq_rope_desc):
         super().__init__(rot_dim, int(bool(interleaved)), _opt_ptr(inv_freq), _opt_ptr(q_weight), _opt_ptr(k_weight),
                          eps)
         self.tensors = (inv_freq, q_weight, k_weight)
+        sizes = {t.numel() for t in (q_weight, k_weight) if t is not None}
+        if len(sizes) > 1:
+            raise ValueError("q_weight and k_weight differ in length")
+        self.head_dim = sizes.pop() if sizes else None
+        self.ref = ctypes.byref(self)
 
 
 class ScoreOpts(kvq_score_opts):
@@ -389,6 +412,7 @@ class ScoreOpts(kvq_score_opts):
             raise ValueError("alibi must be contiguous float32")
         super().__init__(softcap, _opt_ptr(alibi), window, scale)
         self.alibi_tensor = alibi
+        self.ref = ctypes.byref(self)
 
 
 # ------------------------------------------------------------------ convenience owner
@@ -427,6 +451,7 @@ class Cache:
         self.ws_ptr = (base + 255) // 256 * 256
         kvq_bind(self.h, self.ws_ptr, self.nbytes)
         self.B, self.Hkv, self.Hq, self.D = batch, n_kv_heads, n_q_heads, head_dim
+        self._dev, self._bf16, self._f32, self._i32 = self.ws.device, torch.bfloat16, torch.float32, torch.int32
 
     def append(self, layer, K, V, stream=None):
         assert K.is_contiguous() and V.is_contiguous() and K.shape == V.shape
@@ -464,61 +489,74 @@ class Cache:
         return kvq_seq_lens(self.h, layer, self.B)
 
     # -------- steps of several tokens, score shapes, reading back
-    def _tensor(self, t, name, shape, dtype=None):
+    # (these calls are a few microseconds of kernel time at small sizes: the checks below keep to
+    # plain attribute comparisons)
+    def _tensor(self, t, name, shape, dtype):
         """Check one tensor argument: shape, type, device, contiguity."""
-        import torch
-        dtype = dtype or torch.bfloat16
-        if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        if t.shape != shape or t.dtype != dtype:
             raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-        if t.device != self.ws.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {self.ws.device}")
+        if t.device != self._dev:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self._dev}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
-    def _out(self, t, name, shape, dtype=None):
+    def _on_device(self):
+        """Context that makes the cache's device current (nothing to do when it is)."""
         import torch
-        if t is None:
-            return torch.empty(shape, dtype=dtype or torch.bfloat16, device=self.ws.device)
-        self._tensor(t, name, shape, dtype)
-        return t
-
-    def _head_weights(self, rope):
-        for t, name in ((rope.tensors[1], "q_weight"), (rope.tensors[2], "k_weight")):
-            if t is not None and t.numel() != self.D:
-                raise ValueError(f"{name} must have head_dim = {self.D} entries")
-
-    def _slopes(self, opts):
-        if opts is not None and opts.alibi_tensor is not None and opts.alibi_tensor.numel() != self.Hq:
-            raise ValueError(f"alibi must have one slope per query head ({self.Hq})")
+        if self._dev.type != "cuda" or torch.cuda.current_device() == self._dev.index:
+            return _NO_CONTEXT
+        return torch.cuda.device(self._dev)
 
     def norm_rope(self, layer, qkv, rope, offset=None, q=None, K=None, V=None, stream=None):
         """qkv bf16 [B, n, (Hq + 2 Hkv) * D] (rows may be padded); rope a Rope; offset int32
         [B, n] positions behind the cached tokens, None: 0 .. n - 1.  Returns (q [B, n, Hq, D],
         K, V [B, Hkv, n, D])."""
-        import torch
-        if qkv.dim() != 3 or qkv.shape[0] != self.B or qkv.shape[2] != (self.Hq + 2 * self.Hkv) * self.D:
-            raise ValueError(f"qkv: expected [{self.B}, n, {(self.Hq + 2 * self.Hkv) * self.D}], got {tuple(qkv.shape)}")
-        if qkv.dtype != torch.bfloat16 or qkv.stride(2) != 1 or qkv.device != self.ws.device:
+        B, D, row = self.B, self.D, (self.Hq + 2 * self.Hkv) * self.D
+        shape = qkv.shape
+        if len(shape) != 3 or shape[0] != B or shape[2] != row:
+            raise ValueError(f"qkv: expected [{B}, n, {row}], got {tuple(shape)}")
+        bs, ts, cs = qkv.stride()
+        if qkv.dtype != self._bf16 or cs != 1 or qkv.device != self._dev:
             raise ValueError("qkv must be bfloat16 on the cache's device with adjacent channels")
-        n = qkv.shape[1]
+        n = shape[1]
         if offset is not None:
-            self._tensor(offset, "offset", (self.B, n), torch.int32)
-        self._head_weights(rope)
-        with torch.cuda.device(self.ws.device):
-            q = self._out(q, "q", (self.B, n, self.Hq, self.D))
-            K = self._out(K, "K", (self.B, self.Hkv, n, self.D))
-            V = self._out(V, "V", (self.B, self.Hkv, n, self.D))
-            # a dimension of size 1 may carry any stride: give the packed one
-            row = (self.Hq + 2 * self.Hkv) * self.D
-            ts = qkv.stride(1) if n > 1 else row
-            bs = qkv.stride(0) if self.B > 1 else 0
+            self._tensor(offset, "offset", (B, n), self._i32)
+        if rope.head_dim not in (None, D):
+            raise ValueError(f"norm weights must have head_dim = {D} entries")
+        sq, sk = (B, n, self.Hq, D), (B, self.Hkv, n, D)
+        # a dimension of size 1 may carry any stride: give the packed one
+        ts = ts if n > 1 else row
+        bs = bs if B > 1 else 0
+        with self._on_device():
+            if q is None:
+                q = qkv.new_empty(sq)
+            else:
+                self._tensor(q, "q", sq, self._bf16)
+            if K is None:
+                K = qkv.new_empty(sk)
+            else:
+                self._tensor(K, "K", sk, self._bf16)
+            if V is None:
+                V = qkv.new_empty(sk)
+            else:
+                self._tensor(V, "V", sk, self._bf16)
             kvq_norm_rope(self.h, layer, qkv, bs, ts, n, offset, rope, q, K, V, stream)
         return q, K, V
 
     def tree_workspace(self, T):
         """Workspace for tree_attn with T drafted tokens (uint8, 256-byte aligned)."""
         import torch
-        return torch.empty(kvq_tree_attn_workspace_bytes(self.h, T), dtype=torch.uint8, device=self.ws.device)
+        return torch.empty(kvq_tree_attn_workspace_bytes(self.h, T), dtype=torch.uint8, device=self._dev)
+
+    def _attn_out(self, out, like, shape, out_fp32):
+        if out is None:
+            return like.new_empty(shape, dtype=self._f32) if out_fp32 else like.new_empty(shape)
+        self._tensor(out, "out", shape, self._f32 if out_fp32 else self._bf16)
+        return out
+
+    def _slopes(self, opts):
+        if opts is not None and opts.alibi_tensor is not None and opts.alibi_tensor.numel() != self.Hq:
+            raise ValueError(f"alibi must have one slope per query head ({self.Hq})")
 
     def tree_attn(self, layer, q, K, V, n_draft=None, mask=None, depth=None, opts=None, out=None, out_fp32=False,
                   workspace=None, stream=None):
@@ -527,20 +565,20 @@ class Cache:
         ScoreOpts.  workspace: one that tree_workspace(T) gave; calls that may overlap (other
         streams, captured graphs) need one each.  Rows of a fresh `out` behind n_draft[b] are
         unset."""
-        import torch
-        T = q.shape[1]
-        self._tensor(q, "q", (self.B, T, self.Hq, self.D))
-        self._tensor(K, "K", (self.B, self.Hkv, T, self.D))
-        self._tensor(V, "V", (self.B, self.Hkv, T, self.D))
-        if n_draft is not None and len(n_draft) != self.B:
-            raise ValueError(f"n_draft must have {self.B} entries")
+        B, T = self.B, q.shape[1]
+        sq, sk = (B, T, self.Hq, self.D), (B, self.Hkv, T, self.D)
+        self._tensor(q, "q", sq, self._bf16)
+        self._tensor(K, "K", sk, self._bf16)
+        self._tensor(V, "V", sk, self._bf16)
+        if n_draft is not None and len(n_draft) != B:
+            raise ValueError(f"n_draft must have {B} entries")
         if mask is not None:
-            self._tensor(mask, "mask", (self.B, T, (T + 31) // 32), torch.int32)
+            self._tensor(mask, "mask", (B, T, (T + 31) // 32), self._i32)
         if depth is not None:
-            self._tensor(depth, "depth", (self.B, T), torch.int32)
+            self._tensor(depth, "depth", (B, T), self._i32)
         self._slopes(opts)
-        with torch.cuda.device(self.ws.device):
-            out = self._out(out, "out", (self.B, T, self.Hq, self.D), torch.float32 if out_fp32 else torch.bfloat16)
+        with self._on_device():
+            out = self._attn_out(out, q, sq, out_fp32)
             ws = self.tree_workspace(T) if workspace is None else workspace
             if workspace is None and stream is not None and not isinstance(stream, int):
                 ws.record_stream(stream)   # the call's own workspace outlives the launches on `stream`
@@ -549,33 +587,40 @@ class Cache:
 
     def decode_attn_scored(self, layer, q, opts=None, out=None, out_fp32=False, stream=None):
         """decode_attn with capped scores, distance bias or a sliding window (a ScoreOpts)."""
-        import torch
-        self._tensor(q, "q", (self.B, self.Hq, self.D))
+        shape = (self.B, self.Hq, self.D)
+        self._tensor(q, "q", shape, self._bf16)
         self._slopes(opts)
-        with torch.cuda.device(self.ws.device):
-            out = self._out(out, "out", (self.B, self.Hq, self.D), torch.float32 if out_fp32 else torch.bfloat16)
+        with self._on_device():
+            out = self._attn_out(out, q, shape, out_fp32)
             kvq_decode_attn_scored(self.h, layer, q, opts, out, out_fp32, stream)
         return out
 
     def append_selected(self, layer, K, V, index, n_new=None, stream=None):
         """Append slots index[b, :n_new[b]] (int32 [B, n_max]) of K, V [B, Hkv, n_src, D]."""
-        import torch
-        n_src = K.shape[2]
-        self._tensor(K, "K", (self.B, self.Hkv, n_src, self.D))
-        self._tensor(V, "V", (self.B, self.Hkv, n_src, self.D))
-        self._tensor(index, "index", (self.B, index.shape[-1]), torch.int32)
+        n_src, n_max = K.shape[2], index.shape[-1]
+        sk = (self.B, self.Hkv, n_src, self.D)
+        self._tensor(K, "K", sk, self._bf16)
+        self._tensor(V, "V", sk, self._bf16)
+        self._tensor(index, "index", (self.B, n_max), self._i32)
         if n_new is not None and len(n_new) != self.B:
             raise ValueError(f"n_new must have {self.B} entries")
-        with torch.cuda.device(self.ws.device):
-            kvq_append_selected(self.h, layer, K, V, n_src, index, n_new, index.shape[1], stream)
+        with self._on_device():
+            kvq_append_selected(self.h, layer, K, V, n_src, index, n_new, n_max, stream)
 
     def read(self, layer, t0, n, K=None, V=None, stream=None):
         """Tokens [t0, t0 + n) as bf16 (K, V [B, Hkv, n, D]); rows behind a shorter sequence's
         last token are left as they were."""
         import torch
-        with torch.cuda.device(self.ws.device):
-            K = self._out(K, "K", (self.B, self.Hkv, n, self.D))
-            V = self._out(V, "V", (self.B, self.Hkv, n, self.D))
+        sk = (self.B, self.Hkv, n, self.D)
+        with self._on_device():
+            if K is None:
+                K = torch.empty(sk, dtype=self._bf16, device=self._dev)
+            else:
+                self._tensor(K, "K", sk, self._bf16)
+            if V is None:
+                V = torch.empty(sk, dtype=self._bf16, device=self._dev)
+            else:
+                self._tensor(V, "V", sk, self._bf16)
             kvq_read(self.h, layer, t0, n, K, V, stream)
         return K, V
 
