@@ -56,6 +56,11 @@ struct BodyCtx {
     bool row_g, row_g8;
     uint32_t m_hi;
     float unscale, qsum_g, qsum_g8, pbias;
+    // shaped scores (kvq_decode_attn_scored): factor to log2 units (unscale is then 1), cap in
+    // log2 units (0: none) and 2 / cap, slope in log2 units, last token, first token seen, first
+    // token of the block
+    float sfac, cap2, icap, slope2;
+    int pos, lo, tok0;
 };
 
 template <int D, int NT>
@@ -220,7 +225,8 @@ __device__ __forceinline__ void acc_init(WarpAcc<D, NT> &A) {
 // TAIL blocks take their keys from the bf16 residual).
 // PAIR: R holds two 16-token pages (per-token keys), one per half, each laid out
 // [K codes][K scales/zeros][V codes][V scales/zeros], instead of one 32-token record.
-template <int BK, int BV, int KM, int D, int NT, int NH, bool TAIL, bool PAIR = false, int NHP = NH>
+// SHAPED: scores are capped, biased and masked before the softmax (BodyCtx).
+template <int BK, int BV, int KM, int D, int NT, int NH, bool TAIL, bool PAIR = false, int NHP = NH, bool SHAPED = false>
 __device__ __forceinline__ void process_unit(WarpAcc<D, NT> &A, const uint8_t *R, const int valid,
                                              const BodyCtx &c) {
     constexpr int KS = D / 16;
@@ -367,6 +373,22 @@ __device__ __forceinline__ void process_unit(WarpAcc<D, NT> &A, const uint8_t *R
 #pragma unroll
             for (int x = 0; x < 2; ++x)
                 if (8 * n + 2 * t + x >= valid) raw[n][x] = -INFINITY;
+    }
+
+    if constexpr (SHAPED) {
+        // this lane's first token of the block: the others' distances follow by exact subtraction
+        const int tok = c.tok0 + 2 * t, skip = c.lo - tok;
+        const float dist = static_cast<float>(c.pos - tok);
+#pragma unroll
+        for (int n = 0; n < NTI; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float s = raw[n][x] * c.sfac;
+                // cap tanh(s / cap) = cap - 2 cap / (exp(2 s / cap) + 1), in log2 units
+                if (c.cap2 > 0.f) s = fmaf(-2.f * c.cap2, __fdividef(1.f, fast_exp2(s * c.icap) + 1.f), c.cap2);
+                s = fmaf(-c.slope2, dist - static_cast<float>(8 * n + x), s);
+                raw[n][x] = 8 * n + x < skip || (TAIL && 8 * n + 2 * t + x >= valid) ? -INFINITY : s;
+            }
     }
 
     // ===== online softmax (base 2; p carries the factor 2^kp) =====
@@ -926,8 +948,10 @@ __device__ __forceinline__ void patch_stage(uint8_t *stage, int u, const uint8_t
 // ------------------------------------------------------------------ per-layer kernel
 // FUSED: the instance for kvq_append_decode launches (p.k_new set); decode-only launches
 // take the instance without the append code.
-template <int BK, int BV, int KM, int D, int NT, bool FUSED>
+// SHAPED: the instance for kvq_decode_attn_scored (capped, biased or windowed scores).
+template <int BK, int BV, int KM, int D, int NT, bool FUSED, bool SHAPED>
 __global__ void __launch_bounds__(NW * 32, NT == 1 ? 4 : 3) decode_split_kernel(const DecodeParams p) {
+    static_assert(!(FUSED && SHAPED), "shaped scores are not fused with an append");
     const bool early = p.early != 0;   // CTA-uniform
     if (!early) pdl_enter();
     constexpr int REC = unit_bytes(D, BK, BV, KM, 2);
@@ -940,7 +964,9 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 4 : 3) decode_split_kernel(
     const int NS = p.nstage + (warp < p.nextra ? 1 : 0);
     const int sbase = warp * p.nstage + min(warp, p.nextra);
     const int nblk = (L + 31) >> 5;
-    const int blk0 = sp * p.bps, blk1 = min(nblk, blk0 + p.bps);
+    // a window's splits start at its first block (every one of its blocks holds a token that is seen)
+    const int first_tok = SHAPED && p.window ? max(L - p.window, 0) : 0;
+    const int blk0 = (first_tok >> 5) + sp * p.bps, blk1 = min(nblk, blk0 + p.bps);
     const int rem = L & 31;
     const int tail_blk = rem ? (L >> 5) : -1;
 
@@ -1022,6 +1048,15 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 4 : 3) decode_split_kernel(
     setup_query<KM, D, NT>(q_s + hh * D, smax_k, sm.aq_s, sm.scal_s, c, warp);
     __syncthreads();
     load_query_scalars(c, sm.scal_s);
+    if constexpr (SHAPED) {
+        c.sfac = c.unscale * p.rescale;
+        c.unscale = 1.f;
+        c.cap2 = p.cap * kLog2e;
+        c.icap = p.cap > 0.f ? 2.f / p.cap : 0.f;
+        c.slope2 = p.alibi ? p.alibi[h * G + hh] * kLog2e : 0.f;
+        c.pos = L - 1;
+        c.lo = first_tok;
+    }
     // the value prescale must cover the new token's scales: every warp bounds them from
     // the new row (the same CTA-uniform result; the row has arrived: warp 0 waited for it)
     if (append_here) {
@@ -1068,7 +1103,8 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 4 : 3) decode_split_kernel(
             failed = true;
             break;
         }
-        process_unit<BK, BV, KM, D, NT, 2, false>(A, pipe_front(P), 32, c);
+        if constexpr (SHAPED) c.tok0 = 32 * (blk0 + warp + NW * i);
+        process_unit<BK, BV, KM, D, NT, 2, false, false, 2, SHAPED>(A, pipe_front(P), 32, c);
         pipe_pop(P);
         if (P.issued < nb) issue_block(P.issued);
     }
@@ -1095,8 +1131,9 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 4 : 3) decode_split_kernel(
             const bool patch = append_here && tail_blk == new_blk;
             if (patch)
                 patch_stage<BK, BV, KM, D>(const_cast<uint8_t *>(pipe_front(P)), (L - 1) & 31, append_scratch, lane);
-            if (rem <= 16) process_unit<BK, BV, KM, D, NT, 2, true, false, 1>(A, pipe_front(P), rem, c);
-            else process_unit<BK, BV, KM, D, NT, 2, true>(A, pipe_front(P), rem, c);
+            if constexpr (SHAPED) c.tok0 = 32 * tail_blk;
+            if (rem <= 16) process_unit<BK, BV, KM, D, NT, 2, true, false, 1, SHAPED>(A, pipe_front(P), rem, c);
+            else process_unit<BK, BV, KM, D, NT, 2, true, false, 2, SHAPED>(A, pipe_front(P), rem, c);
             ++i;
         }
     }
@@ -1255,10 +1292,10 @@ __global__ void merge_kernel(const MergeParams p) {
 
 using KernelFn = void (*)(const DecodeParams);
 
-template <int D, int NT, int KM, bool FUSED>
+template <int D, int NT, int KM, bool FUSED, bool SHAPED>
 KernelFn pick_bits(int bk, int bv) {
 #define KVQ_CASE(BKv, BVv) \
-    if (bk == BKv && bv == BVv) return decode_split_kernel<BKv, BVv, KM, D, NT, FUSED>;
+    if (bk == BKv && bv == BVv) return decode_split_kernel<BKv, BVv, KM, D, NT, FUSED, SHAPED>;
     KVQ_CASE(2, 2) KVQ_CASE(2, 4) KVQ_CASE(2, 8)
     KVQ_CASE(4, 2) KVQ_CASE(4, 4) KVQ_CASE(4, 8)
     KVQ_CASE(8, 2) KVQ_CASE(8, 4) KVQ_CASE(8, 8)
@@ -1271,24 +1308,25 @@ KernelFn pick_bits(int bk, int bv) {
 // tiles otherwise.
 static int nt_for(int G) { return (G == 1 || G == 2 || G == 4) ? 1 : 2; }
 
-template <bool FUSED>
+template <bool FUSED, bool SHAPED>
 KernelFn pick_kernel_t(int D, int bk, int bv, int kmode, int G) {
     const int NT = nt_for(G);
     if (G < 1 || G > 8) return nullptr;
     if (kmode == 1) {
         // rows (group, head) must fit one 16-row tile and heads must divide 8
         if (!(G == 1 || G == 2 || G == 4) || G * (D / 32) > 16) return nullptr;
-        if (D == 64) return pick_bits<64, 1, 1, FUSED>(bk, bv);
-        if (D == 128) return pick_bits<128, 1, 1, FUSED>(bk, bv);
+        if (D == 64) return pick_bits<64, 1, 1, FUSED, SHAPED>(bk, bv);
+        if (D == 128) return pick_bits<128, 1, 1, FUSED, SHAPED>(bk, bv);
         return nullptr;
     }
-    if (D == 64) return NT == 1 ? pick_bits<64, 1, 0, FUSED>(bk, bv) : pick_bits<64, 2, 0, FUSED>(bk, bv);
-    if (D == 128) return NT == 1 ? pick_bits<128, 1, 0, FUSED>(bk, bv) : pick_bits<128, 2, 0, FUSED>(bk, bv);
+    if (D == 64) return NT == 1 ? pick_bits<64, 1, 0, FUSED, SHAPED>(bk, bv) : pick_bits<64, 2, 0, FUSED, SHAPED>(bk, bv);
+    if (D == 128) return NT == 1 ? pick_bits<128, 1, 0, FUSED, SHAPED>(bk, bv) : pick_bits<128, 2, 0, FUSED, SHAPED>(bk, bv);
     return nullptr;
 }
 
-KernelFn pick_kernel(int D, int bk, int bv, int kmode, int G, bool fused) {
-    return fused ? pick_kernel_t<true>(D, bk, bv, kmode, G) : pick_kernel_t<false>(D, bk, bv, kmode, G);
+KernelFn pick_kernel(int D, int bk, int bv, int kmode, int G, bool fused, bool shaped) {
+    if (shaped) return pick_kernel_t<false, true>(D, bk, bv, kmode, G);
+    return fused ? pick_kernel_t<true, false>(D, bk, bv, kmode, G) : pick_kernel_t<false, false>(D, bk, bv, kmode, G);
 }
 
 }  // namespace
@@ -1320,7 +1358,7 @@ struct KernelState {
     int occ[8] = {};
 };
 static std::mutex g_state_mu;
-static KernelState g_state[160];   // every decode instance (2 x 54), the paged and merge kernels
+static KernelState g_state[192];   // every decode instance (3 x 54), the paged and merge kernels
 
 static cudaError_t prepare_kernel(const void *fn, size_t smem, int *occ_out) {
     std::lock_guard<std::mutex> lk(g_state_mu);
@@ -1358,7 +1396,7 @@ static cudaError_t prepare_kernel(const void *fn, size_t smem, int *occ_out) {
 
 cudaError_t decode_occupancy(int D, int bk, int bv, int kmode, int G, long long rec_bytes, int nstage,
                              int nextra, int *ctas_per_sm) {
-    KernelFn fn = pick_kernel(D, bk, bv, kmode, G, false);   // the fused instance has the same occupancy
+    KernelFn fn = pick_kernel(D, bk, bv, kmode, G, false, false);   // the other instances have the same occupancy
     if (!fn) return cudaErrorInvalidValue;
     return prepare_kernel(reinterpret_cast<const void *>(fn), decode_smem_bytes(rec_bytes, nstage, nextra, D, G),
                           ctas_per_sm);
@@ -1366,7 +1404,7 @@ cudaError_t decode_occupancy(int D, int bk, int bv, int kmode, int G, long long 
 
 cudaError_t launch_decode(const DecodeParams &p, int D, int bk, int bv, int kmode, cudaStream_t st,
                           int *ctas_per_sm_out) {
-    KernelFn fn = pick_kernel(D, bk, bv, kmode, p.G, p.k_new != nullptr);
+    KernelFn fn = pick_kernel(D, bk, bv, kmode, p.G, p.k_new != nullptr, p.shaped != 0);
     if (!fn) return cudaErrorInvalidValue;
     const size_t smem = decode_smem_bytes(p.rec_bytes, p.nstage, p.nextra, D, p.G);
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(fn), smem, ctas_per_sm_out);

@@ -717,10 +717,10 @@ static int ensure_device_info(kvq_handle *h) {
 // prefetch depth).
 // Split count S, stages per warp and extra stages (for the warps with the most blocks
 // when one stage per warp is used) of a per-layer decode launch.
-static int splits_for(kvq_handle *h, int layer, int *S_out, int *nstage_out, int *nextra_out) {
+// nblk: blocks of the longest sequence that the launch reads (0: all of them).
+static int splits_for(kvq_handle *h, int layer, int *S_out, int *nstage_out, int *nextra_out, int nblk = 0) {
     const LayerGeom &g = h->geom[layer];
-    const int L = h->len[layer];
-    const int nblk = (L + 31) / 32;
+    if (nblk == 0) nblk = (h->len[layer] + 31) / 32;
     const int G = h->desc.n_q_heads / h->desc.n_kv_heads;
     const int ns_max = kvq::decode_stages(g.rec_bytes, h->desc.head_dim, G);
     int rc = ensure_device_info(h);
@@ -1538,8 +1538,8 @@ int check_score_opts(const kvq_score_opts *o) {
 
 long long tree_table_bytes(const kvq_handle *h) { return align256(8LL * h->desc.batch); }
 
-// Launch parameters that kvq_tree_attn and kvq_decode_attn_scored share, and the split of
-// the sequence: nk drafted keys at most per request.
+// Launch parameters of kvq_tree_attn, and the split of the sequence: nk drafted keys at most
+// per request.
 void tree_params(kvq_handle *h, int layer, const kvq_score_opts *o, int T, int nk, int max_splits, kvq::TreeParams &p) {
     const LayerGeom &g = h->geom[layer];
     p.rec = h->ws + g.rec_off;
@@ -1715,20 +1715,65 @@ int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_sc
     if ((rc = check_score_opts(opts))) return rc;
     for (int b = 0; b < h->desc.batch; ++b)
         if (h->rlen[layer][b] < 1) return fail(KVQ_EINVAL, "layer %d: request %d is empty", layer, b);
+    const float D = static_cast<float>(h->desc.head_dim);
+    const float scale = opts && opts->scale != 0.f ? opts->scale : 1.f / std::sqrt(D);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    kvq::TreeParams p{};
-    const int G = h->desc.n_q_heads / h->desc.n_kv_heads;
-    tree_params(h, layer, opts, 1, 0, std::min(kvq::kMaxSplits, kvq::tree_max_splits(h->desc.batch, h->desc.n_kv_heads, G)),
-                p);
+    const LayerGeom &g = h->geom[layer];
+    const int window = opts ? opts->window : 0;
+    // blocks of the longest sequence, or those a window can reach into
+    int nblk = (h->len[layer] + 31) / 32;
+    if (window) nblk = static_cast<int>(std::min<long long>(nblk, (static_cast<long long>(window) + 31) / 32 + 1));
+    int S = 1, nstage = 2, nextra = 0;
+    if ((rc = splits_for(h, layer, &S, &nstage, &nextra, nblk))) return rc;
+    kvq::DecodeParams p{};
+    p.rec = h->ws + g.rec_off;
+    p.res = g.res_off >= 0 ? reinterpret_cast<const uint16_t *>(h->ws + g.res_off) : nullptr;
     p.q = static_cast<const uint16_t *>(q);
+    p.smax = smax_slot(h, layer, static_cast<int>(h->ver[layer]));
+    if ((rc = fill_lengths(h, layer, p, 0, st))) return rc;
     p.out = out;
-    p.out_fp32 = out_fp32 ? 1 : 0;
-    p.pos0 = -1;
     p.part_acc = reinterpret_cast<float *>(h->ws + h->part_acc_off);
     p.part_ml = reinterpret_cast<float *>(h->ws + h->part_ml_off);
     p.sstride = kvq::kMaxSplits;
-    if ((rc = fill_seq_lens(h, layer, p.len, 1, nullptr, lens_table(h, layer), st))) return rc;
-    return tree_launch(h, p, st);
+    p.status = reinterpret_cast<unsigned *>(h->ws + h->status_off);
+    p.B = h->desc.batch;
+    p.Hkv = h->desc.n_kv_heads;
+    p.G = h->desc.n_q_heads / h->desc.n_kv_heads;
+    p.L = h->len[layer];
+    p.cap_blk = h->cap_blk;
+    p.bps = (nblk + S - 1) / S;
+    p.S = (nblk + p.bps - 1) / p.bps;
+    p.out_fp32 = out_fp32 ? 1 : 0;
+    p.nstage = nstage;
+    p.nextra = nextra;
+    p.rec_bytes = g.rec_bytes;
+    p.btab = block_table(h, layer);
+    p.arrive = p.S >= kvq::kInLaunchMergeSplits ? reinterpret_cast<unsigned *>(h->ws + h->arrive_off) : nullptr;
+    p.shaped = 1;
+    p.rescale = scale * std::sqrt(D);
+    p.cap = opts ? opts->softcap : 0.f;
+    p.alibi = opts ? opts->alibi : nullptr;
+    p.window = window;
+    if ((rc = prepare_status(h, st))) return rc;
+    cudaError_t e = kvq::launch_decode(p, h->desc.head_dim, g.bk, g.bv, g.kmode, st, nullptr);
+    if (e != cudaSuccess) return cuda_fail(e, "scored decode launch");
+    note_write(h, st, -1);
+    if (p.S > 1 && !p.arrive) {
+        kvq::MergeParams m{};
+        m.part_acc = p.part_acc;
+        m.part_ml = p.part_ml;
+        m.out = out;
+        m.B = p.B;
+        m.Hq = h->desc.n_q_heads;
+        m.D = h->desc.head_dim;
+        m.S = p.S;
+        m.out_fp32 = p.out_fp32;
+        m.sstride = p.sstride;
+        e = kvq::launch_merge(m, st);
+        if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+        note_write(h, st, -1);
+    }
+    return ok();
 }
 
 int kvq_append_selected(kvq_handle *h, int layer, const void *K, const void *V, int n_src, const int32_t *index,

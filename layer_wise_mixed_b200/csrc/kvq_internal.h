@@ -138,6 +138,14 @@ struct DecodeParams {
     // in the stream writes none of this layer's records or residual (see pdl_enter)
     int early;
     const int *btab;            // block pools: [B][cap_blk] pool block of each block (rec is the pool)
+    // kvq_decode_attn_scored (shaped != 0; never fused): scores times rescale (the call's scale
+    // over 1 / sqrt(D)), capped at cap (0: none), minus alibi[hq] (or null) times the distance to
+    // the last token; window (0: none) as the number of last tokens that are seen.  Splits are
+    // cut from the window's first block on.
+    int shaped;
+    float rescale, cap;
+    const float *alibi;
+    int window;
 };
 
 
@@ -224,13 +232,13 @@ struct SeqLens {
 #endif
 };
 
-// Attention of T query tokens per request over the packed cache and (kd != null) over the
-// T drafted tokens themselves (kvq_tree_attn, kvq_decode_attn_scored).
+// Attention of T drafted tokens per request over the packed cache and over one another
+// (kvq_tree_attn).
 struct TreeParams {
     const uint8_t *rec;         // layer records
     const uint16_t *res;        // residual (per-channel keys) or null
     const uint16_t *q;          // bf16 [B][T][Hq][D]
-    const uint16_t *kd, *vd;    // bf16 [B][Hkv][T][D], or null: cached tokens only
+    const uint16_t *kd, *vd;    // bf16 [B][Hkv][T][D]
     const uint32_t *mask;       // [B][T][mask_words], or null: token t sees tokens 0 .. t
     const int *depth;           // [B][T] position of token t behind the cached ones, or null: t
     const float *alibi;         // [Hq] slopes, or null
@@ -244,7 +252,6 @@ struct TreeParams {
     int B, Hkv, G, T, cap_blk, mask_words;
     int S;                      // splits of every request's tiles (even parts)
     unsigned gmul;              // ceil(2^32 / G) (x / G = mulhi(x, gmul) for x < 2^29), 0 for G = 1
-    int pos0;                   // query position - cached length - depth (0; -1: the last cached token)
     int window;                 // 0: none
     float cap, scale;           // cap 0: none; scale of q . k
     int out_fp32;

@@ -1,6 +1,5 @@
 // Attention of several query tokens per request over the packed cache and over the drafted
-// tokens themselves (kvq_tree_attn), and of one query token with score shapes
-// (kvq_decode_attn_scored), on the 5th-generation tensor cores (sm_100a).
+// tokens themselves (kvq_tree_attn), on the 5th-generation tensor cores (sm_100a).
 //
 //   s = scale q.k^,  s = cap tanh(s / cap),  s -= slope (pos_q - pos_k);  out = softmax(s) v^
 //
@@ -505,7 +504,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     fence_after();
     const uint32_t tmem = bar->tmem;
     // query positions; the earliest one's window bounds the tiles
-    auto query_pos = [&](int r) { return L + p.pos0 + (p.kd ? (depth ? depth[row_t(r)] : row_t(r)) : 0); };
+    auto query_pos = [&](int r) { return L + (depth ? depth[row_t(r)] : row_t(r)); };
     if (p.window) {
         if (tid < nrow) atomicMin(&bar->min_pos, query_pos(tid));
         __syncthreads();
@@ -513,7 +512,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     // open keys: places for the open key group, then drafted tokens (a chunk: those up to the
     // last row)
     const int open = p.kmode == 0 ? L & 31 : 0, pad = open ? 32 : 0;
-    const int nk = !p.kd ? 0 : (p.mask ? nq : min(nq, row_t(nrow - 1) + 1));
+    const int nk = p.mask ? nq : min(nq, row_t(nrow - 1) + 1);
     const int n_open = (pad + nk + kTile - 1) / kTile;
     const int nblk = (L - open + 31) >> 5;                    // packed blocks
     int tile_first = 0;
