@@ -334,7 +334,10 @@ KVQ_API int kvq_tag_allocate(int num_tags, const double *D2, const double *D4, c
  * A step that verifies drafted tokens, or feeds a prompt in chunks, runs
  *   kvq_norm_rope -> kvq_tree_attn -> (the caller accepts tokens) -> kvq_append_selected
  * per layer.  The pages describe none of these; they are this library's own additions
- * around the pages' cache. */
+ * around the pages' cache.  Outputs may not overlap inputs.  As elsewhere, calls on one
+ * handle share the bound workspace (batches above 64: the layer's length table; split
+ * partials): order them on the GPU when they go to different streams.  kvq_tree_attn keeps
+ * its partials and tables in the workspace passed to it. */
 
 /* Norm and rotation of a projection's rows. */
 typedef struct {
@@ -381,10 +384,11 @@ typedef struct {
  * NULL: T each): request b has its first n_draft[b] tokens; output rows from there on are
  * left as they were, and the values behind them in q, K, V and mask have no influence.
  * Requests may be empty (length 0).  A row that sees no key comes out as zeros; a key that
- * a row does not see has no influence on it, whatever K and V hold there.  Cached and
- * drafted values are taken as fp16 where they enter the second product (drafted values
- * beyond its range saturate, as they would in the cache, unless infinite); scores,
- * softmax and sums are fp32.  T <= 4096.  workspace: device memory of
+ * a row does not see has no influence on it, whatever K and V hold there.  Depths are >= 0,
+ * positions below 2^31.
+ * Accuracy: cached keys and values and the softmax weights enter the products rounded to
+ * fp16 (2^-11 of each at most; drafted values beyond fp16's range saturate, as they would in
+ * the cache, unless infinite); scores, softmax and sums are fp32.  T <= 4096.  workspace: device memory of
  * kvq_tree_attn_workspace_bytes, 256-byte aligned, owned by the call until it has run.
  * One launch, and a merge launch when the sequence is split. */
 KVQ_API int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const void *V, int T,
@@ -396,8 +400,9 @@ KVQ_API int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K
 KVQ_API int kvq_tree_attn_workspace_bytes(const kvq_handle *h, int T, size_t *bytes);
 
 /* kvq_decode_attn with opts: one query token per request (q, out [B][Hq][D]) over all
- * cached tokens of `layer`; the query's position is that of the last cached token.  Split
- * partials live in the bound workspace.  Every request must hold a token. */
+ * cached tokens of `layer`; the query's position is that of the last cached token.  The
+ * kernel, its accuracy and its splits are those of kvq_decode_attn on its default path; with
+ * a window, only the blocks it reaches are read.  Every request must hold a token. */
 KVQ_API int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_score_opts *opts, void *out,
                                    int out_fp32, void *stream);
 

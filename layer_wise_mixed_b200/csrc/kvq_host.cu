@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <new>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -1588,12 +1589,17 @@ int tree_launch(kvq_handle *h, kvq::TreeParams &p, cudaStream_t st) {
 
 constexpr int kMaxDraft = 4096;
 
+// Host memory for a call's bookkeeping ran out (no exception may cross the C boundary).
+int no_memory() {
+    return fail(KVQ_EINVAL, "out of host memory");
+}
+
 }  // namespace
 
 extern "C" {
 
 int kvq_norm_rope(kvq_handle *h, int layer, const void *qkv, int64_t batch_stride, int64_t token_stride, int n,
-                  const int32_t *offset, const kvq_rope_desc *rope, void *q, void *K, void *V, void *stream) {
+                  const int32_t *offset, const kvq_rope_desc *rope, void *q, void *K, void *V, void *stream) try {
     int rc = check_layer(h, layer);
     if (rc) return rc;
     if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_norm_rope");
@@ -1639,6 +1645,8 @@ int kvq_norm_rope(kvq_handle *h, int layer, const void *qkv, int64_t batch_strid
     if (e != cudaSuccess) return cuda_fail(e, "norm + rotation launch");
     note_write(h, st, -1);
     return ok();
+} catch (const std::bad_alloc &) {
+    return no_memory();
 }
 
 int kvq_tree_attn_workspace_bytes(const kvq_handle *h, int T, size_t *bytes) {
@@ -1657,7 +1665,7 @@ int kvq_tree_attn_workspace_bytes(const kvq_handle *h, int T, size_t *bytes) {
 
 int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const void *V, int T, const int32_t *n_draft,
                   const uint32_t *mask, const int32_t *depth, const kvq_score_opts *opts, void *out, int out_fp32,
-                  void *workspace, size_t workspace_bytes, void *stream) {
+                  void *workspace, size_t workspace_bytes, void *stream) try {
     int rc = check_layer(h, layer);
     if (rc) return rc;
     if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_tree_attn");
@@ -1684,6 +1692,8 @@ int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const 
     if (!aligned(workspace, 256)) return fail(KVQ_EALIGN, "workspace must be 256-byte aligned");
     if (nq_max == 0) return ok();
     const int G = h->desc.n_q_heads / h->desc.n_kv_heads;
+    if (static_cast<long long>(h->desc.n_kv_heads) * kvq::tree_row_groups(T * G) > 65535)
+        return fail(KVQ_EUNSUPPORTED, "too many query rows for one launch");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     kvq::TreeParams p{};
     const int S = kvq::tree_max_splits(B, h->desc.n_kv_heads, T * G);
@@ -1702,10 +1712,12 @@ int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const 
     p.sstride = S;
     if ((rc = fill_seq_lens(h, layer, p.len, T, n_draft, reinterpret_cast<int *>(ws), st))) return rc;
     return tree_launch(h, p, st);
+} catch (const std::bad_alloc &) {
+    return no_memory();
 }
 
 int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_score_opts *opts, void *out, int out_fp32,
-                           void *stream) {
+                           void *stream) try {
     int rc = check_layer(h, layer);
     if (rc) return rc;
     if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_decode_attn_scored");
@@ -1774,10 +1786,12 @@ int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_sc
         note_write(h, st, -1);
     }
     return ok();
+} catch (const std::bad_alloc &) {
+    return no_memory();
 }
 
 int kvq_append_selected(kvq_handle *h, int layer, const void *K, const void *V, int n_src, const int32_t *index,
-                        const int32_t *n_new, int n_max, void *stream) {
+                        const int32_t *n_new, int n_max, void *stream) try {
     int rc = check_layer(h, layer);
     if (rc) return rc;
     if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_append_selected");
@@ -1785,9 +1799,11 @@ int kvq_append_selected(kvq_handle *h, int layer, const void *K, const void *V, 
     if (!aligned(index, 4)) return fail(KVQ_EALIGN, "index must be 4-byte aligned");
     if (n_src < 1) return fail(KVQ_EINVAL, "n_src must be >= 1 (got %d)", n_src);
     return append_impl(h, layer, K, V, n_new, n_max, stream, index, n_src);
+} catch (const std::bad_alloc &) {
+    return no_memory();
 }
 
-int kvq_read(kvq_handle *h, int layer, int t0, int n, void *K, void *V, void *stream) {
+int kvq_read(kvq_handle *h, int layer, int t0, int n, void *K, void *V, void *stream) try {
     int rc = check_layer(h, layer);
     if (rc) return rc;
     if (h->desc.paged) return fail(KVQ_EUNSUPPORTED, "paged plans are not supported by kvq_read");
@@ -1817,6 +1833,8 @@ int kvq_read(kvq_handle *h, int layer, int t0, int n, void *K, void *V, void *st
     if (e != cudaSuccess) return cuda_fail(e, "read launch");
     note_write(h, st, -1);
     return ok();
+} catch (const std::bad_alloc &) {
+    return no_memory();
 }
 
 }  // extern "C"
