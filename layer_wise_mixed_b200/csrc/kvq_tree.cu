@@ -31,7 +31,7 @@
 //   token u of block w: u = 16 kk + 8 ch + 2 t + hb   ->  64 (w / 2) + 16 t + 8 (w % 2) + 4 kk + 2 ch + hb
 //
 // Measured (Llama shape, 8 kv heads, 4 query heads each): 64 drafted tokens at batch 16, context
-// 32768, K4V4: 0.70 ms, 0.79 PFLOP/s, 47% of the measured bf16 rate; 16 drafted tokens at batch
+// 32768, K4V4: 0.71 ms, 0.78 PFLOP/s, 46% of the measured bf16 rate; 16 drafted tokens at batch
 // 64, context 4096, K4V2: 213 us (padded to 128 rows, the MMAs alone would take 63 us, the bytes
 // 44 us).  What bounds it: the issue of the unpack and softmax warps.  The tensor pipe is active 29%
 // of the cycles, 46% of issue slots are used, and the stall that leads among warps that could
