@@ -336,7 +336,9 @@ KVQ_API int kvq_tag_allocate(int num_tags, const double *D2, const double *D4, c
  * per layer.  The pages describe none of these; they are this library's own additions
  * around the pages' cache.  Outputs may not overlap inputs.  As elsewhere, calls on one
  * handle share the bound workspace (batches above 64: the layer's length table; split
- * partials): order them on the GPU when they go to different streams.  kvq_tree_attn keeps
+ * partials): order them on the GPU when they go to different streams.  The first call that
+ * launches after kvq_bind also clears the library's words in the workspace and cannot be
+ * captured into a graph (KVQ_EINVAL from kvq_tree_attn and kvq_append_selected).  kvq_tree_attn keeps
  * its partials and tables in the workspace passed to it. */
 
 /* Norm and rotation of a projection's rows. */

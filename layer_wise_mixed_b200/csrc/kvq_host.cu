@@ -196,6 +196,18 @@ int prepare_status(kvq_handle *h, cudaStream_t st) {
     return KVQ_OK;
 }
 
+// The first launch after a bind clears the status word and the layers' scale maxima; captured
+// into a graph, every replay would clear them again.
+int first_launch_not_captured(const kvq_handle *h, cudaStream_t st) {
+    if (h->status_clear) return KVQ_OK;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(st, &cs);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    if (cs != cudaStreamCaptureStatusNone)
+        return fail(KVQ_EINVAL, "the first call after kvq_bind cannot be captured into a graph");
+    return KVQ_OK;
+}
+
 int cuda_fail(cudaError_t e, const char *what) {
     return fail(KVQ_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -529,6 +541,7 @@ int append_impl(kvq_handle *h, int layer, const void *K, const void *V, const in
     p.nV = static_cast<int>(nV);
     p.nK = static_cast<int>(nK);
     if (p.nV == 0) return ok();          // no token appended: nothing changes (the slot neither)
+    if (index && (rc = first_launch_not_captured(h, static_cast<cudaStream_t>(stream)))) return rc;
     std::vector<int> bidx, bval;         // block pools: new table entries
     {
         std::vector<int> L_new(B);
@@ -1695,6 +1708,7 @@ int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const 
     if (static_cast<long long>(h->desc.n_kv_heads) * kvq::tree_row_groups(T * G) > 65535)
         return fail(KVQ_EUNSUPPORTED, "too many query rows for one launch");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = first_launch_not_captured(h, st))) return rc;
     kvq::TreeParams p{};
     const int S = kvq::tree_max_splits(B, h->desc.n_kv_heads, T * G);
     tree_params(h, layer, opts, T, nq_max, S, p);

@@ -265,3 +265,71 @@ def test_long_context():
     mask, depth = ref.random_tree(1, 24, 31)
     c.check(mask=mask, depth=depth, what="long")
     c.check(mask=mask, depth=depth, window=7001, what="long window")
+
+
+def test_first_call_is_not_captured():
+    """The first launch after a bind clears the workspace's words: refused inside a capture
+    (a replay would clear them again), fine once something ran."""
+    c = Case([0, 0], 4, seed=50)
+    ws = c.cache.tree_workspace(4)
+    out = torch.zeros_like(c.q)
+    index = torch.zeros((2, 1), dtype=torch.int32, device="cuda")
+    for call in (lambda: c.cache.tree_attn(0, c.q, c.Kd, c.Vd, out=out, workspace=ws),
+                 lambda: c.cache.append_selected(0, c.Kd, c.Vd, index)):
+        with pytest.raises(kvq.KvqError) as e:
+            with torch.cuda.graph(torch.cuda.CUDAGraph()):
+                call()
+        assert e.value.code == kvq.KVQ_EINVAL and "captured" in str(e.value)
+    c.check(what="after the refusals")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.cache.tree_attn(0, c.q, c.Kd, c.Vd, out=out, workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, c.cache.tree_attn(0, c.q, c.Kd, c.Vd))
+
+
+def test_largest_draft():
+    """4096 tokens of a causal chunk over a short prefix: rows picked over the chunk."""
+    c = Case([75], 4096, Hkv=1, G=8, D=64, bits=(8, 8), seed=51)
+    out = c.cache.tree_attn(0, c.q, c.Kd, c.Vd, out_fp32=True)
+    Kh, Vh = ref.cached_values(c.K[0], c.V[0], 75, 8, 8, 0)
+    f = lambda x: x.double().cpu().numpy()
+    pos = 75 + np.arange(4096.0)
+    rows = [0, 1, 15, 16, 31, 32, 127, 2047, 2048, 4080, 4095]
+    see = np.tril(np.ones((4096, 4096), bool))[rows]
+    r, e = ref.attention(f(c.q[0])[rows], Kh, Vh, f(c.Kd[0]), f(c.Vd[0]), see, pos[rows], pos, 75, 8)
+    ref.check(out[0, rows], r, e, "T=4096")
+    assert torch.isfinite(out).all() and kvq.kvq_device_status(c.cache.h) == 0
+
+
+@pytest.mark.slow
+def test_cache_beyond_four_gigabytes():
+    """Records whose offsets pass 32 bits (32 units of 960,000 tokens, K8V8: 4.4 GB): tree
+    attention, scored decode and read-back of the last unit."""
+    B, Hkv, D, L, step = 4, 8, 64, 960000, 60000
+    cache = kvq.Cache(1, B, Hkv, Hkv, D, L, [(8, 8)])
+    last = []
+    for i in range(L // step):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        K, V = (torch.randn((B, Hkv, step, D), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        cache.append(0, K, V)
+        last.append((K[-1, -1:].cpu(), V[-1, -1:].cpu()))
+    assert cache.nbytes > 1 << 32
+    K, V = (torch.cat([x[k] for x in last], 1) for k in (0, 1))
+    Kh, Vh = ref.cached_values(K, V, L, 8, 8, 0)
+    T = 3
+    g = torch.Generator(device="cuda").manual_seed(99)
+    q, Kd, Vd = (torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+                 for s in ((B, T, Hkv, D), (B, Hkv, T, D), (B, Hkv, T, D)))
+    out = cache.tree_attn(0, q, Kd, Vd, out_fp32=True)
+    f = lambda x: x.double().cpu().numpy()
+    pos = L + np.arange(float(T))
+    r, e = ref.attention(f(q[-1, :, -1:]), Kh, Vh, f(Kd[-1, -1:]), f(Vd[-1, -1:]), np.tril(np.ones((T, T), bool)), pos, pos, L, 1)
+    ref.check(out[-1, :, -1:], r, e, "tree")
+    o = cache.decode_attn_scored(0, q[:, 0].contiguous(), kvq.ScoreOpts(20.0), out_fp32=True)
+    r, e = ref.attention(f(q[-1, :1, -1:]), Kh, Vh, None, None, None, np.array([L - 1.0]), None, L, 1, cap=20.0)
+    ref.check(o[-1:, -1:], r, e, "scored")
+    Ko, Vo = cache.read(0, L - 500, 500)
+    as_bf16 = lambda x: torch.from_numpy(x).float().to(torch.bfloat16)
+    assert torch.equal(Ko[-1, -1].cpu(), as_bf16(Kh[0, -500:])) and torch.equal(Vo[-1, -1].cpu(), as_bf16(Vh[0, -500:]))
