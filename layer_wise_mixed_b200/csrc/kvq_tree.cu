@@ -682,7 +682,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const uint8_t *src = p.rec + (is_v ? key_part : 0);
         const uint32_t ring = smem_u32(ring_of(is_v)), on = elect_one();
         bool lap = false;      // every stage has been used
-        for (int i = 0, st = 0, ph = 0; i < n; ++i) {
+        int st = 0, ph = 0;
+        for (int i = 0; i < n; ++i) {
             int blk0;
             const int nb = blocks_of(is_v, i, blk0);
             if (nb <= 0) continue;
@@ -697,6 +698,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                              &bar->part_full[is_v][st]);
             if (++st == stages) st = 0, ph ^= 1, lap = true;
         }
+        // no copy is in flight when the CTA ends, whatever wait expired before: each used stage's
+        // last phase (stages below st were filled in this lap, the others in the one before)
+        Waiter drain;
+        for (int k = 0; k < (lap ? stages : st); ++k) drain(&bar->part_full[is_v][k], k < st ? ph : ph ^ 1);
+        wait.failed |= drain.failed;
       } else if (warp == 16 && n > 0) {
         // ================================================================ MMA issue
         {
@@ -746,6 +752,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                     pv(j, i, i / STEP, i + STEP >= n);
                     if (i + STEP < n) qk(j, i + STEP);
                 }
+            // nor is an MMA in flight when tensor memory is freed
+            Waiter drain;
+            drain(&bar->o_full[0], 0);
+            if (TWO || n > 1) drain(&bar->o_full[1], 0);
+            wait.failed |= drain.failed;
         }
         __syncwarp();
       }
