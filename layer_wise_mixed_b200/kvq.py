@@ -146,6 +146,16 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _torch_stream(stream, device):
+    """The torch stream of a Stream object or of a raw handle on `device`."""
+    import torch
+    if not isinstance(stream, int):
+        return stream
+    if stream in (0, 1):   # the legacy default stream's two handles
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(stream, device=device)
+
+
 def _ptr(x) -> int:
     return x if isinstance(x, int) else x.data_ptr()
 
@@ -463,20 +473,26 @@ class Cache:
         kvq_append_tagged(self.h, layer, K, V, K.shape[2], tags.cpu().numpy(), tags, stream)
 
     def decode_attn(self, layer, q, out=None, out_fp32=False, stream=None):
-        import torch
         if out is None:
-            out = torch.empty((self.B, self.Hq, self.D), dtype=torch.float32 if out_fp32 else torch.bfloat16,
-                              device=q.device)
+            out = self._decode_out(q, out_fp32, stream)
         kvq_decode_attn(self.h, layer, q, out, out_fp32, stream)
+        return out
+
+    def _decode_out(self, q, out_fp32, stream):
+        """A fresh output of a decode step that runs on `stream`."""
+        dtype = self._f32 if out_fp32 else self._bf16
+        if stream is None:
+            return q.new_empty((self.B, self.Hq, self.D), dtype=dtype)
+        with self._on(stream):
+            out = q.new_empty((self.B, self.Hq, self.D), dtype=dtype)
+        self._hand_over(stream, out)
         return out
 
     def append_decode(self, layer, K, V, q, out=None, out_fp32=False, stream=None):
         """One decode step: append the token K, V [B, Hkv, 1, D] and attend with q."""
-        import torch
         assert K.is_contiguous() and V.is_contiguous() and K.shape == V.shape and K.shape[2] == 1
         if out is None:
-            out = torch.empty((self.B, self.Hq, self.D), dtype=torch.float32 if out_fp32 else torch.bfloat16,
-                              device=q.device)
+            out = self._decode_out(q, out_fp32, stream)
         kvq_append_decode(self.h, layer, K, V, q, out, out_fp32, stream)
         return out
 
@@ -500,12 +516,28 @@ class Cache:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
-    def _on_device(self):
-        """Context that makes the cache's device current (nothing to do when it is)."""
+    def _on(self, stream):
+        """Context of a call: the cache's device and `stream` (None: the current one) are current
+        in it, so that what a call allocates belongs to the stream that the call runs on."""
         import torch
+        if stream is not None:
+            s = _torch_stream(stream, self._dev)
+            if s.device != self._dev:
+                raise ValueError(f"stream is on {s.device}, the cache on {self._dev}")
+            return torch.cuda.stream(s)
         if self._dev.type != "cuda" or torch.cuda.current_device() == self._dev.index:
             return _NO_CONTEXT
         return torch.cuda.device(self._dev)
+
+    def _hand_over(self, stream, *fresh):
+        """Tensors that a call on `stream` allocated go to a caller whose current stream may be
+        another: their memory is not reused before that stream's work at the time they are freed
+        has run, either."""
+        if stream is not None:
+            import torch
+            cur = torch.cuda.current_stream(self._dev)
+            for t in fresh:
+                t.record_stream(cur)
 
     def norm_rope(self, layer, qkv, rope, offset=None, q=None, K=None, V=None, stream=None):
         """qkv bf16 [B, n, (Hq + 2 Hkv) * D] (rows may be padded); rope a Rope; offset int32
@@ -527,7 +559,7 @@ class Cache:
         # a dimension of size 1 may carry any stride: give the packed one
         ts = ts if n > 1 else row
         bs = bs if B > 1 else 0
-        with self._on_device():
+        with self._on(stream):
             if q is None:
                 q = qkv.new_empty(sq)
             else:
@@ -540,7 +572,8 @@ class Cache:
                 V = qkv.new_empty(sk)
             else:
                 self._tensor(V, "V", sk, self._bf16)
-            kvq_norm_rope(self.h, layer, qkv, bs, ts, n, offset, rope, q, K, V, stream)
+            kvq_norm_rope(self.h, layer, qkv, bs, ts, n, offset, rope, q, K, V)
+        self._hand_over(stream, q, K, V)
         return q, K, V
 
     def tree_workspace(self, T):
@@ -577,12 +610,12 @@ class Cache:
         if depth is not None:
             self._tensor(depth, "depth", (B, T), self._i32)
         self._slopes(opts)
-        with self._on_device():
+        with self._on(stream):
             out = self._attn_out(out, q, sq, out_fp32)
+            # (a workspace of the call's own is memory of the call's stream: reused in its order)
             ws = self.tree_workspace(T) if workspace is None else workspace
-            if workspace is None and stream is not None and not isinstance(stream, int):
-                ws.record_stream(stream)   # the call's own workspace outlives the launches on `stream`
-            kvq_tree_attn(self.h, layer, q, K, V, T, n_draft, mask, depth, opts, out, out_fp32, ws, ws.numel(), stream)
+            kvq_tree_attn(self.h, layer, q, K, V, T, n_draft, mask, depth, opts, out, out_fp32, ws, ws.numel())
+        self._hand_over(stream, out)
         return out
 
     def decode_attn_scored(self, layer, q, opts=None, out=None, out_fp32=False, stream=None):
@@ -590,9 +623,10 @@ class Cache:
         shape = (self.B, self.Hq, self.D)
         self._tensor(q, "q", shape, self._bf16)
         self._slopes(opts)
-        with self._on_device():
+        with self._on(stream):
             out = self._attn_out(out, q, shape, out_fp32)
-            kvq_decode_attn_scored(self.h, layer, q, opts, out, out_fp32, stream)
+            kvq_decode_attn_scored(self.h, layer, q, opts, out, out_fp32)
+        self._hand_over(stream, out)
         return out
 
     def append_selected(self, layer, K, V, index, n_new=None, stream=None):
@@ -604,15 +638,15 @@ class Cache:
         self._tensor(index, "index", (self.B, n_max), self._i32)
         if n_new is not None and len(n_new) != self.B:
             raise ValueError(f"n_new must have {self.B} entries")
-        with self._on_device():
-            kvq_append_selected(self.h, layer, K, V, n_src, index, n_new, n_max, stream)
+        with self._on(stream):
+            kvq_append_selected(self.h, layer, K, V, n_src, index, n_new, n_max)
 
     def read(self, layer, t0, n, K=None, V=None, stream=None):
         """Tokens [t0, t0 + n) as bf16 (K, V [B, Hkv, n, D]); rows behind a shorter sequence's
         last token are left as they were."""
         import torch
         sk = (self.B, self.Hkv, n, self.D)
-        with self._on_device():
+        with self._on(stream):
             if K is None:
                 K = torch.empty(sk, dtype=self._bf16, device=self._dev)
             else:
@@ -621,7 +655,8 @@ class Cache:
                 V = torch.empty(sk, dtype=self._bf16, device=self._dev)
             else:
                 self._tensor(V, "V", sk, self._bf16)
-            kvq_read(self.h, layer, t0, n, K, V, stream)
+            kvq_read(self.h, layer, t0, n, K, V)
+        self._hand_over(stream, K, V)
         return K, V
 
     def truncate(self, layer, L):
