@@ -407,6 +407,10 @@ class Rope(kvq_rope_desc):
         super().__init__(rot_dim, int(bool(interleaved)), _opt_ptr(inv_freq), _opt_ptr(q_weight), _opt_ptr(k_weight),
                          eps)
         self.tensors = (inv_freq, q_weight, k_weight)
+        devices = {t.device for t in self.tensors if t is not None}
+        if len(devices) > 1:
+            raise ValueError("inv_freq and weights are on different devices")
+        self.device = devices.pop() if devices else None   # (norm_rope compares it with the cache's)
         sizes = {t.numel() for t in (q_weight, k_weight) if t is not None}
         if len(sizes) > 1:
             raise ValueError("q_weight and k_weight differ in length")
@@ -520,12 +524,14 @@ class Cache:
         """Context of a call: the cache's device and `stream` (None: the current one) are current
         in it, so that what a call allocates belongs to the stream that the call runs on."""
         import torch
-        if stream is not None:
+        if stream is not None and self._dev.type == "cuda":
             s = _torch_stream(stream, self._dev)
             if s.device != self._dev:
                 raise ValueError(f"stream is on {s.device}, the cache on {self._dev}")
             return torch.cuda.stream(s)
-        if self._dev.type != "cuda" or torch.cuda.current_device() == self._dev.index:
+        if self._dev.type != "cuda":
+            raise ValueError(f"the cache is on {self._dev}: kernels need a CUDA device")
+        if torch.cuda.current_device() == self._dev.index:
             return _NO_CONTEXT
         return torch.cuda.device(self._dev)
 
@@ -555,6 +561,8 @@ class Cache:
             self._tensor(offset, "offset", (B, n), self._i32)
         if rope.head_dim not in (None, D):
             raise ValueError(f"norm weights must have head_dim = {D} entries")
+        if rope.device not in (None, self._dev):
+            raise ValueError(f"inv_freq and weights are on {rope.device}, the cache on {self._dev}")
         sq, sk = (B, n, self.Hq, D), (B, self.Hkv, n, D)
         # a dimension of size 1 may carry any stride: give the packed one
         ts = ts if n > 1 else row
@@ -588,8 +596,11 @@ class Cache:
         return out
 
     def _slopes(self, opts):
-        if opts is not None and opts.alibi_tensor is not None and opts.alibi_tensor.numel() != self.Hq:
-            raise ValueError(f"alibi must have one slope per query head ({self.Hq})")
+        if opts is not None and opts.alibi_tensor is not None:
+            if opts.alibi_tensor.numel() != self.Hq:
+                raise ValueError(f"alibi must have one slope per query head ({self.Hq})")
+            if opts.alibi_tensor.device != self._dev:
+                raise ValueError(f"alibi is on {opts.alibi_tensor.device}, the cache on {self._dev}")
 
     def tree_attn(self, layer, q, K, V, n_draft=None, mask=None, depth=None, opts=None, out=None, out_fp32=False,
                   workspace=None, stream=None):
@@ -610,11 +621,14 @@ class Cache:
         if depth is not None:
             self._tensor(depth, "depth", (B, T), self._i32)
         self._slopes(opts)
+        if workspace is not None and (workspace.device != self._dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous memory of {self._dev}")
         with self._on(stream):
             out = self._attn_out(out, q, sq, out_fp32)
             # (a workspace of the call's own is memory of the call's stream: reused in its order)
             ws = self.tree_workspace(T) if workspace is None else workspace
-            kvq_tree_attn(self.h, layer, q, K, V, T, n_draft, mask, depth, opts, out, out_fp32, ws, ws.numel())
+            kvq_tree_attn(self.h, layer, q, K, V, T, n_draft, mask, depth, opts, out, out_fp32, ws,
+                          ws.numel() * ws.element_size())
         self._hand_over(stream, out)
         return out
 
