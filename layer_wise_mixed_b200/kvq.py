@@ -347,8 +347,14 @@ def _host_i32(x):
     """(address, array kept alive) of an optional host int32 array."""
     if x is None:
         return None, None
-    a = array.array("i", x) if isinstance(x, (list, tuple)) else np.ascontiguousarray(x, np.int32)
-    return (a.buffer_info()[0] if isinstance(a, array.array) else a.ctypes.data), a
+    if isinstance(x, (list, tuple)):
+        a = array.array("i", x)   # (raises for fractions and for what int32 does not hold)
+        return a.buffer_info()[0], a
+    x = np.asarray(x)
+    a = np.ascontiguousarray(x, np.int32)
+    if x.dtype.kind not in "iu" or (a != x).any():
+        raise ValueError("counts must be integers that int32 holds")
+    return a.ctypes.data, a
 
 
 def _ref(s):
