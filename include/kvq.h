@@ -369,7 +369,7 @@ KVQ_API int kvq_norm_rope(kvq_handle *h, int layer, const void *qkv, int64_t bat
  * then s -= alibi[hq] * (position of q - position of k); a key is seen only if position of
  * q - position of k < window.  All-zero (or a NULL pointer to it): plain attention. */
 typedef struct {
-    float softcap;         /* 0: none; else > 0 */
+    float softcap;         /* 0: none; else > 0, finite: off by 2^-20 of a cap up to 64, by 2^-18 of the score above */
     const float *alibi;    /* device fp32 [n_q_heads], or NULL */
     int window;            /* 0: none; else >= 1 */
     float scale;           /* 0: 1 / sqrt(head_dim) */

@@ -384,8 +384,8 @@ __device__ __forceinline__ void process_unit(WarpAcc<D, NT> &A, const uint8_t *R
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float s = raw[n][x] * c.sfac;
-                // cap tanh(s / cap) = cap - 2 cap / (exp(2 s / cap) + 1), in log2 units
-                if (c.cap2 > 0.f) s = fmaf(-2.f * c.cap2, __fdividef(1.f, fast_exp2(s * c.icap) + 1.f), c.cap2);
+                if (c.cap2 > kWideCap * kLog2e) s = capped_wide(s, c.cap2, c.icap);
+                else if (c.cap2 > 0.f) s = capped(s, c.cap2, c.icap);
                 s = fmaf(-c.slope2, dist - static_cast<float>(8 * n + x), s);
                 raw[n][x] = 8 * n + x < skip || (TAIL && 8 * n + 2 * t + x >= valid) ? -INFINITY : s;
             }

@@ -141,6 +141,28 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float fast_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// cap tanh(s / cap) = cap - 2 cap / (exp(2 s / cap) + 1) of a score s in log2 units, cap2 = cap
+// log2(e), icap = 2 / cap.  The difference cancels where |s| is far below the cap: its error is
+// 2^-20 of the cap at most, whatever s is.  Caps above kWideCap take capped_wide.
+constexpr float kWideCap = 64.f;
+__device__ __forceinline__ float capped(float s, float cap2, float icap) {
+    return fmaf(-2.f * cap2, fast_rcp(fast_exp2(s * icap) + 1.f), cap2);
+}
+// The same with an error of 2^-18 of the score at most: below x = |s / cap| = 1/4 the series
+// tanh(x) = x (1 - x^2/3 + 2 x^4/15 - 17 x^6/315 + 62 x^8/2835) (next term: 2^-26), where the
+// result is a quarter of the cap or more the form above.
+__device__ __forceinline__ float capped_wide(float s, float cap2, float icap) {
+    const float x = s * (icap * 0.34657359f), y = x * x;   // s / cap: ln(2) / 2 undoes the units
+    const float near = s * fmaf(y, fmaf(y, fmaf(y, fmaf(y, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+    return fabsf(x) < 0.25f ? near : capped(s, cap2, icap);
+}
+
 // Load a lane's words of one half code area (Wh words, chunked by min(4, Wh)).
 template <int WH>
 __device__ __forceinline__ void load_lane_words(const uint8_t *half_area, int lane, uint32_t *w) {

@@ -1550,6 +1550,13 @@ int check_score_opts(const kvq_score_opts *o) {
     return KVQ_OK;
 }
 
+// The cap that the kernels use.  Outside [1e-20, 1e30] it changes no fp32 result: a smaller cap
+// leaves every weight one, a larger one every score as it is.  The bounds keep the kernels' 2 /
+// cap and cap log2(e) finite.
+float kernel_cap(const kvq_score_opts *o) {
+    return o && o->softcap > 0.f ? std::min(std::max(o->softcap, 1e-20f), 1e30f) : 0.f;
+}
+
 long long tree_table_bytes(const kvq_handle *h) { return align256(8LL * h->desc.batch); }
 
 // Launch parameters of kvq_tree_attn, and the split of the sequence: nk drafted keys at most
@@ -1568,7 +1575,7 @@ void tree_params(kvq_handle *h, int layer, const kvq_score_opts *o, int T, int n
     p.gmul = p.G > 1 ? static_cast<unsigned>(((1ull << 32) + p.G - 1) / p.G) : 0u;
     p.cap_blk = h->cap_blk;
     p.mask_words = (T + 31) / 32;
-    p.cap = o ? o->softcap : 0.f;
+    p.cap = kernel_cap(o);
     p.alibi = o ? o->alibi : nullptr;
     p.window = o ? o->window : 0;
     p.scale = o && o->scale != 0.f ? o->scale : 1.f / std::sqrt(static_cast<float>(h->desc.head_dim));
@@ -1777,7 +1784,7 @@ int kvq_decode_attn_scored(kvq_handle *h, int layer, const void *q, const kvq_sc
     p.arrive = p.S >= kvq::kInLaunchMergeSplits ? reinterpret_cast<unsigned *>(h->ws + h->arrive_off) : nullptr;
     p.shaped = 1;
     p.rescale = scale * std::sqrt(D);
-    p.cap = opts ? opts->softcap : 0.f;
+    p.cap = kernel_cap(opts);
     p.alibi = opts ? opts->alibi : nullptr;
     p.window = window;
     if ((rc = prepare_status(h, st))) return rc;

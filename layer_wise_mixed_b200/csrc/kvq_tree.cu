@@ -263,11 +263,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-__device__ __forceinline__ float fast_rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ uint32_t hfma2_bits(uint32_t c, uint32_t s, uint32_t z) {
     return h2_bits(__hfma2(bits_h2(c), bits_h2(s), bits_h2(z)));
@@ -844,13 +839,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         }
                     }
                     const float f = is_open ? 1.f : rs;
-                    if (p.cap > 0.f) {
-                        // cap tanh(s / cap) = cap - 2 cap / (exp(2 s / cap) + 1), in log2 units
-                        const float c2 = p.cap * kLog2eT, fc = f * (2.f / p.cap);
+                    if (p.cap > kWideCap) {
+                        const float c2 = p.cap * kLog2eT, ic = 2.f / p.cap;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            x[e] = __float_as_uint(
-                                fmaf(-2.f * c2, fast_rcp(fast_exp2(__uint_as_float(x[e]) * fc) + 1.f), c2));
+                            x[e] = __float_as_uint(capped_wide(__uint_as_float(x[e]) * f, c2, ic));
+                    } else if (p.cap > 0.f) {
+                        // (raw scores, with the row's factor in the exponent's; kept finite: 0 times it is 0)
+                        const float c2 = p.cap * kLog2eT, fc = fminf(f * (2.f / p.cap), 3e38f);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(capped(__uint_as_float(x[e]), c2, fc));
                     } else if (!is_open && !p.alibi) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
