@@ -1122,22 +1122,27 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     float M = -INFINITY;
     for (int s = 0; s < p.S; ++s) M = fmaxf(M, ml[s].x);
     constexpr int PER = D / 32;
-    float o[PER], den = 0.f;
+    // NaN and infinities that a row sees are added at full weight, as in a launch without splits: a
+    // weight of zero must not meet them
+    float o[PER], bad[PER], den = 0.f;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    for (int e = 0; e < PER; ++e) o[e] = bad[e] = 0.f;
     for (int s = 0; s < p.S; ++s) {
         const float2 v = ml[s];
-        // a split without a visible key holds zeros (or NaN and infinite values that are seen)
-        const float w = v.x == -INFINITY ? 1.f : fast_exp2(v.x - M);
-        den = fmaf(w, v.y, den);
+        const float w = v.x == -INFINITY ? 0.f : fast_exp2(v.x - M);   // 0: a split without a visible key
+        den += v.x == -INFINITY ? v.y : w * v.y;
         const float *a = p.part_acc + (row * p.sstride + s) * D + PER * lane;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] = fmaf(w, a[e], o[e]);
+        for (int e = 0; e < PER; ++e) {
+            const bool fin = fabsf(a[e]) < INFINITY;
+            o[e] = fmaf(w, fin ? a[e] : 0.f, o[e]);
+            bad[e] += fin ? 0.f : a[e];
+        }
     }
     const float n = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
     for (int e = 0; e < PER; e += 2) {
-        const float x = o[e] * n, y = o[e + 1] * n;
+        const float x = fmaf(o[e], n, bad[e]), y = fmaf(o[e + 1], n, bad[e + 1]);
         const long long at = row * D + PER * lane + e;
         if (p.out_fp32) *reinterpret_cast<float2 *>(static_cast<float *>(p.out) + at) = make_float2(x, y);
         else *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = __floats2bfloat162_rn(x, y);
