@@ -388,9 +388,11 @@ typedef struct {
  * Requests may be empty (length 0).  A row that sees no key comes out as zeros; a key that
  * a row does not see has no influence on it, whatever K and V hold there.  Depths are >= 0,
  * positions below 2^31.
- * Accuracy: cached keys and values and the softmax weights enter the products rounded to
- * fp16 (2^-11 of each at most; drafted values beyond fp16's range saturate, as they would in
- * the cache, unless infinite); scores, softmax and sums are fp32.  T <= 4096.  workspace: device memory of
+ * Accuracy: cached keys and values, drafted values and the softmax weights enter the products
+ * rounded to fp16 (2^-11 of each at most); scores, softmax and sums are fp32.  Drafted values
+ * beyond 65504 saturate there, unless infinite.  A layer with a group whose |zero| + scale
+ * (2^b - 1) is above 65504 is computed scaled by 2^-e to fp16's range (e <= 10): its values are then
+ * off by up to 2^(e + b - 25) instead, if that is more.  T <= 4096.  workspace: device memory of
  * kvq_tree_attn_workspace_bytes, 256-byte aligned, owned by the call until it has run.
  * One launch, and a merge launch when the sequence is split. */
 KVQ_API int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const void *V, int T,

@@ -46,7 +46,7 @@ __device__ __forceinline__ int src_slot(const AppendParams &p, int unit, int i) 
 // Per-token quantization of the new tokens of one 16-token half-block and repacking
 // of its words.  role 0 = keys (per-token mode), 1 = values.
 __device__ void per_token_half(const AppendParams &p, int role, int unit, int hbi, int L_old, int n,
-                               uint8_t (*codes)[kMaxD], unsigned *cta_smax) {
+                               uint8_t (*codes)[kMaxD], unsigned *cta_smax, unsigned *cta_top) {
     const int D = p.D, nj = D / 32;
     const int bits = role ? p.bv : p.bk;
     const uint16_t *src = (role ? p.V : p.K) + static_cast<long long>(unit) * p.n_src * D;
@@ -93,6 +93,7 @@ __device__ void per_token_half(const AppendParams &p, int role, int unit, int hb
                 *reinterpret_cast<uint16_t *>(sz + so) = s16;
                 *reinterpret_cast<uint16_t *>(sz + so + 4 * nj) = z16;
                 atomicMax(cta_smax, static_cast<unsigned>(s16));
+                if (const unsigned top = group_top(s, z, bits)) atomicMax(cta_top, top);
             }
         }
     }
@@ -122,7 +123,8 @@ __device__ void per_token_half(const AppendParams &p, int role, int unit, int hb
 // Per-channel quantization of one completed 32-token key group; the CTA with
 // first == true also writes the new residual tokens of its (b, h) afterwards.
 __device__ void per_channel_group(const AppendParams &p, int unit, int q, bool do_group, bool first, int L_old,
-                                  int n, float (*xs)[kMaxD], uint8_t (*codes)[kMaxD], unsigned *cta_smax) {
+                                  int n, float (*xs)[kMaxD], uint8_t (*codes)[kMaxD], unsigned *cta_smax,
+                                  unsigned *cta_top) {
     const int D = p.D;
     const uint16_t *src = p.K + static_cast<long long>(unit) * p.n_src * D;
     uint16_t *res = p.res + static_cast<long long>(unit) * 32 * D;
@@ -150,6 +152,7 @@ __device__ void per_channel_group(const AppendParams &p, int unit, int q, bool d
             *reinterpret_cast<uint16_t *>(rec + p.kc + so) = s16;
             *reinterpret_cast<uint16_t *>(rec + p.kc + so + 4) = z16;
             atomicMax(cta_smax, static_cast<unsigned>(s16));
+            if (const unsigned top = group_top(s, z, p.bk)) atomicMax(cta_top, top);
         }
         __syncthreads();
         const int bits = p.bk, Wh = D * bits / 64, F = 32 / bits, nwh = D * bits / 2;
@@ -181,13 +184,14 @@ __device__ void per_channel_group(const AppendParams &p, int unit, int q, bool d
 
 // Scales are non-negative, so their fp16 bit patterns order like their values: the
 // largest scale of the layer is kept with integer atomicMax (one per CTA), for the
-// decoder's choice of fp16 operand prescales.
+// decoder's choice of fp16 operand prescales; so are the value bounds that leave fp16's range
+// (group_top: hardly ever any).
 __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
     pdl_enter();
     __shared__ __align__(16) float xs[32][kMaxD];
     __shared__ __align__(16) uint8_t codes[32][kMaxD];
-    __shared__ unsigned cta_smax;
-    if (threadIdx.x == 0) cta_smax = 0;
+    __shared__ unsigned cta_smax, cta_top;
+    if (threadIdx.x == 0) cta_smax = cta_top = 0;
     __syncthreads();
     const int cta = blockIdx.x;
     // this CTA's request range: the launch's own, or (ragged) its request's
@@ -215,24 +219,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
         role = 1;
         const int unit = cta / p.nhb, hi = cta % p.nhb;
         range(unit, L_old, n, hb0, nhb, g0, ng);
-        if (hi < nhb) per_token_half(p, 1, unit, hb0 + hi, L_old, n, codes, &cta_smax);
+        if (hi < nhb) per_token_half(p, 1, unit, hb0 + hi, L_old, n, codes, &cta_smax, &cta_top);
     } else {
         role = 0;
         const int k = cta - p.nV;
         if (p.kmode == 1) {
             const int unit = k / p.nhb, hi = k % p.nhb;
             range(unit, L_old, n, hb0, nhb, g0, ng);
-            if (hi < nhb) per_token_half(p, 0, unit, hb0 + hi, L_old, n, codes, &cta_smax);
+            if (hi < nhb) per_token_half(p, 0, unit, hb0 + hi, L_old, n, codes, &cta_smax, &cta_top);
         } else {
             const int per_unit = p.ng > 0 ? p.ng : 1;
             const int unit = k / per_unit, qi = k % per_unit;
             range(unit, L_old, n, hb0, nhb, g0, ng);
             if (qi < ng || qi == 0)
-                per_channel_group(p, unit, g0 + qi, qi < ng, qi == 0, L_old, n, xs, codes, &cta_smax);
+                per_channel_group(p, unit, g0 + qi, qi < ng, qi == 0, L_old, n, xs, codes, &cta_smax,
+                                  &cta_top);
         }
     }
     __syncthreads();
     if (threadIdx.x == 0 && cta_smax) atomicMax(p.smax + role, cta_smax);
+    if (threadIdx.x == 0 && cta_top) atomicMax(p.top + role, cta_top);
     // carry the maxima of the old length into the new length's slot
     if (cta == 0 && threadIdx.x == 0 && p.smax_prev != p.smax) {
         atomicMax(p.smax, p.smax_prev[0]);

@@ -794,16 +794,16 @@ __device__ __forceinline__ void or_token_words(uint32_t *area, int role, int e, 
 // every group at once.  Codes, scales and zeros go to `scratch` (shared memory), from
 // which the warp that processes the block patches its staged copy (patch_stage); the
 // cache in HBM gets them from append_token_store.  Returns the new scale maxima (keys,
-// values; fp16 bits) on every lane.
+// values; fp16 bits) and value bounds above fp16's range (group_top) on every lane.
 template <int BK, int BV, int KM, int D>
 __device__ __forceinline__ void append_token_quantize(uint8_t *scratch, const uint16_t *kn, const uint16_t *vn,
-                                                      int lane, unsigned smax_new[2]) {
+                                                      int lane, unsigned smax_new[2], unsigned top_new[2]) {
     static_assert(D == 64 || D == 128, "head_dim 64 or 128");
     constexpr int NJ = D / 32, CPL = D / 32, LPG = 32 / CPL;
     uint8_t *codes = scratch;                                              // [0, D): values, [D, 2D): keys
     uint16_t *szs = reinterpret_cast<uint16_t *>(scratch + 2 * D + 16);   // [role][j][scale, zero]
     const int j = lane / LPG, d0 = CPL * lane;   // this lane's group and first channel
-    smax_new[0] = smax_new[1] = 0u;
+    smax_new[0] = smax_new[1] = top_new[0] = top_new[1] = 0u;
     constexpr int NROLE = KM == 1 ? 2 : 1;
 #pragma unroll
     for (int r = 0; r < NROLE; ++r) {
@@ -846,6 +846,7 @@ __device__ __forceinline__ void append_token_quantize(uint8_t *scratch, const ui
             szs[(role * NJ + j) * 2 + 1] = z16;
         }
         smax_new[role] = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(s16));
+        top_new[role] = __reduce_max_sync(0xffffffffu, quant::group_top(sc, z, bits));
     }
     __syncwarp();
 }
@@ -867,7 +868,8 @@ __device__ __forceinline__ void append_residual_row(const DecodeParams &p, long 
 // maxima.  One warp.
 template <int BK, int BV, int KM, int D>
 __device__ __forceinline__ void append_token_store(const DecodeParams &p, long long unit, int blk, int u,
-                                                   const uint8_t *scratch, int lane, const unsigned smax_new[2]) {
+                                                   const uint8_t *scratch, int lane, const unsigned smax_new[2],
+                                                   const unsigned top_new[2]) {
     constexpr int NJ = D / 32;
     constexpr int KC = 4 * D * BK, KSZ = 4 * D, VC = 4 * D * BV;
     constexpr int REC = KC + KSZ + VC + 4 * D;
@@ -895,6 +897,8 @@ __device__ __forceinline__ void append_token_store(const DecodeParams &p, long l
     if (lane == 0) {
         if (smax_new[0]) atomicMax(p.smax_out, smax_new[0]);
         if (smax_new[1]) atomicMax(p.smax_out + 1, smax_new[1]);
+        if (top_new[0]) atomicMax(p.top_out, top_new[0]);
+        if (top_new[1]) atomicMax(p.top_out + 1, top_new[1]);
     }
 }
 
@@ -1076,14 +1080,14 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 4 : 3) decode_split_kernel(
         if (warp == helper) {
             // the token's rows (kn, vn) arrive by bulk copy with the q rows
             if (!mbar_wait(pro_bar, 0) && lane == 0) atomicOr(p.status, kStatusWaitExpired);
-            unsigned smax_new[2];
-            append_token_quantize<BK, BV, KM, D>(append_scratch, kn_s, vn_s, lane, smax_new);
+            unsigned smax_new[2], top_new[2];
+            append_token_quantize<BK, BV, KM, D>(append_scratch, kn_s, vn_s, lane, smax_new, top_new);
             // the tail reads the new residual row from HBM after the hand-over; the record's
             // words, scales and the maxima are only for later launches: written after it,
             // so the barrier's release does not wait for them
             if constexpr (KM == 0) append_residual_row<D>(p, unit, (L - 1) & 31, kn_s, lane);
             if (helper != owner) asm volatile("bar.arrive 1, %0;" ::"n"(64) : "memory");
-            append_token_store<BK, BV, KM, D>(p, unit, new_blk, (L - 1) & 31, append_scratch, lane, smax_new);
+            append_token_store<BK, BV, KM, D>(p, unit, new_blk, (L - 1) & 31, append_scratch, lane, smax_new, top_new);
         }
     }
 

@@ -186,6 +186,12 @@ unsigned *smax_slot(const kvq_handle *h, int layer, int parity) {
     return reinterpret_cast<unsigned *>(h->ws + h->smax_off) + 4 * layer + 2 * (parity & 1);
 }
 
+// The layer's {key, value} bounds above fp16's range (group_top), behind all layers' scale maxima.
+// They only grow, and no launch that writes them reads them: one slot.
+unsigned *top_slot(const kvq_handle *h, int layer) {
+    return reinterpret_cast<unsigned *>(h->ws + h->smax_off) + 4 * h->desc.num_layers + 2 * layer;
+}
+
 // The status word and the per-layer maximum scales live in caller memory of unknown
 // content: zero them on the stream of the first launch after a bind.
 int prepare_status(kvq_handle *h, cudaStream_t st) {
@@ -339,7 +345,8 @@ int kvq_plan(const kvq_plan_desc *d, kvq_handle **out) {
     const int D = d->head_dim;
     h->status_off = 0;
     h->smax_off = 256;                                             // after the status word
-    h->arrive_off = align256(256 + 16LL * d->num_layers);         // {K, V} max scale per layer and parity
+    // {K, V} max scale per layer and parity, then {K, V} value bounds per layer
+    h->arrive_off = align256(256 + 24LL * d->num_layers);
     h->meta_bytes = align256(h->arrive_off + 4LL * d->batch * d->n_kv_heads);   // split arrival counters
     long long off = h->meta_bytes;
     // per-request length tables of batches above kvq::kMaxRagged (one per layer, so calls
@@ -486,6 +493,7 @@ int append_impl(kvq_handle *h, int layer, const void *K, const void *V, const in
     p.V = static_cast<const uint16_t *>(V);
     p.smax = smax_slot(h, layer, static_cast<int>(h->ver[layer] + 1));
     p.smax_prev = smax_slot(h, layer, static_cast<int>(h->ver[layer]));
+    p.top = top_slot(h, layer);
     p.rec = h->ws + g.rec_off;
     p.res = g.res_off >= 0 ? reinterpret_cast<uint16_t *>(h->ws + g.res_off) : nullptr;
     p.B = B;
@@ -1112,6 +1120,7 @@ int kvq_append_decode(kvq_handle *h, int layer, const void *K, const void *V, co
     p.rec_w = h->ws + g.rec_off;
     p.res_w = g.res_off >= 0 ? reinterpret_cast<uint16_t *>(h->ws + g.res_off) : nullptr;
     p.smax_out = smax_slot(h, layer, static_cast<int>(h->ver[layer] + 1));
+    p.top_out = top_slot(h, layer);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if ((rc = prepare_status(h, st))) {
         h->len[layer] = L_old;
@@ -1565,7 +1574,7 @@ void tree_params(kvq_handle *h, int layer, const kvq_score_opts *o, int T, int n
     const LayerGeom &g = h->geom[layer];
     p.rec = h->ws + g.rec_off;
     p.res = g.res_off >= 0 ? reinterpret_cast<const uint16_t *>(h->ws + g.res_off) : nullptr;
-    p.smax = smax_slot(h, layer, static_cast<int>(h->ver[layer]));
+    p.top = top_slot(h, layer);
     p.btab = block_table(h, layer);
     p.status = reinterpret_cast<unsigned *>(h->ws + h->status_off);
     p.B = h->desc.batch;

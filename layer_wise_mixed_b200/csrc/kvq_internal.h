@@ -60,6 +60,10 @@ constexpr int kDecodeWarps = 4;     // warps per decode CTA
 // Device status word bits (written with atomicOr, read by kvq_device_status).
 constexpr unsigned kStatusWaitExpired = 1u;   // a bounded mbarrier wait gave up
 constexpr unsigned kStatusBadIndex = 2u;      // kvq_append_selected met an index outside its source
+// Largest finite fp16 number.  A group's values lie within |zero| + scale (2^b - 1); where that
+// bound is larger (finite scale and zero, but a sum that fp16 does not hold) the appends keep the
+// layer's largest one, for kernels whose operands are fp16 values.
+constexpr float kHalfMax = 65504.f;
 // Wall-time limit of one bounded wait inside a kernel (nanoseconds of the GPU's global
 // timer): 100 ms, far above any copy's latency, far below what would hold a GPU.
 constexpr unsigned long long kWaitLimitNs = 100ull * 1000 * 1000;
@@ -79,6 +83,7 @@ struct AppendParams {
                                 // uses its first n_r[b] tokens)
     unsigned *smax;             // {max key scale, max value scale} (fp16 bits) at the new length
     const unsigned *smax_prev;  // the same at the old length (other parity slot), or smax
+    unsigned *top;              // {keys, values}: largest value bounds above kHalfMax (see there)
     uint8_t *rec;               // layer records [B][Hkv][cap][rec_bytes]
     uint16_t *res;              // residual [B][Hkv][32][D] bf16 (per-channel keys)
     int B, Hkv, D, bk, bv, kmode;
@@ -133,6 +138,7 @@ struct DecodeParams {
     uint8_t *rec_w;
     uint16_t *res_w;
     unsigned *smax_out;
+    unsigned *top_out;          // the layer's value bounds (AppendParams::top)
     // early != 0: the first stages' block copies (and the L2 prefetch of the residual
     // rows) are issued before pdl_enter(); the host sets it only when the previous launch
     // in the stream writes none of this layer's records or residual (see pdl_enter)
@@ -242,7 +248,7 @@ struct TreeParams {
     const uint32_t *mask;       // [B][T][mask_words], or null: token t sees tokens 0 .. t
     const int *depth;           // [B][T] position of token t behind the cached ones, or null: t
     const float *alibi;         // [Hq] slopes, or null
-    const unsigned *smax;       // this layer's {max key scale, max value scale} (fp16 bits)
+    const unsigned *top;        // this layer's {key, value} bounds above kHalfMax (float bits), 0: none
     const int *btab;
     void *out;                  // [B][T][Hq][D] bf16 or fp32
     float *part_acc;            // split partials: row r = (b T + t) Hq + hq, slot s: [r][sstride][D]

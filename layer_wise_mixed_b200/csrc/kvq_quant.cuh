@@ -25,6 +25,13 @@ __device__ __forceinline__ void group_params(float mn, float mx, int bits, float
     z16 = __half_as_ushort(zh);
 }
 
+// Float bits of a group's value bound if it is above fp16's range (non-negative floats order like
+// their bits), else 0.
+__device__ __forceinline__ unsigned group_top(float s, float z, int bits) {
+    const float top = fmaf(s, static_cast<float>((1 << bits) - 1), fabsf(z));
+    return top > kHalfMax ? __float_as_uint(top) : 0u;
+}
+
 __device__ __forceinline__ int group_code(float x, float s, float z, int bits) {
     if (s == 0.0f) return 0;
     const int c = __float2int_rn(__fdiv_rn(__fsub_rn(x, z), s));

@@ -43,11 +43,13 @@
 // to one stage).
 //
 // Roundings.  A cached key or value is one fp16 FMA of its exact code: off by 2^-11 of itself
-// at most, and exact where the scale and zero are subnormal.  Query rows and bf16 key rows are
-// scaled by a power of two to below 2^15 (exact in fp16 to 2^-38 of the row's largest);
-// layers whose largest scale would leave fp16's range are scaled down as a whole.  Weights
-// are fp16 of 2^(s - m + 7): m follows the running maximum, and lags by up to 2^8 so that
-// the sums in tensor memory are rescaled only when it grew by more.  Scores, m, l and O are
+// at most, and exact below fp16's normal numbers (code, scale and zero are whole multiples of
+// the step there).  Query rows and bf16 key rows are scaled by a power of two to below 2^15
+// (exact in fp16 to 2^-38 of the row's largest); layers with a value that would leave fp16's
+// range are scaled down as a whole, by 2^e (e = 1 .. 10; a scale or zero below 2^(e-14) is then
+// off by 2^(e-25), so a value by 2^(e+b-25) at most).  Weights are fp16 of 2^(s - m + 7): m
+// follows the running maximum, and lags by up to 2^8 so that the sums in tensor memory are
+// rescaled only when it grew by more; l sums them before that rounding.  Scores, m, l and O are
 // fp32.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -267,8 +269,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint32_t hfma2_bits(uint32_t c, uint32_t s, uint32_t z) {
     return h2_bits(__hfma2(bits_h2(c), bits_h2(s), bits_h2(z)));
 }
-__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b) { return h2_bits(__hmul2(bits_h2(a), bits_h2(b))); }
-
 // W consecutive words (4, 2 or 1) of shared memory.
 template <int W>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
@@ -280,6 +280,19 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t *w) {
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
     }
 }
+// A part's scales and zeros (2 D halves at sz, in shared memory) times f, a power of two: by the warp
+// that unpacks the part, before it does.  A loop over few words rather than a second instance of
+// the unpackers: that one's code beside the others' cost 17% at batch 16, context 32768.
+template <int D>
+__device__ __forceinline__ void scale_part(uint32_t sz, int lane, float f) {
+#pragma unroll 1
+    for (int i = lane; i < D; i += 32) {
+        uint32_t w;
+        lds_words<1>(sz + 4 * i, &w);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sz + 4 * i), "r"(pack_h2(half_lo_f(w) * f, half_hi_f(w) * f)) : "memory");
+    }
+    __syncwarp();
+}
 // Byte offset, within a half's code area, of a lane's words [BITS / 2 * i, ..) : the words of
 // eight consecutive slots (a 32-channel step of keys, a channel group of values).
 template <int BITS, int D>
@@ -290,12 +303,11 @@ __device__ __forceinline__ int step_words(int i, int lane) {
 }
 
 // Key block w of a tile (part: [codes][s/z] in shared memory) -> fp16 rows of the K operand.
-// PRE: scales and zeros times `pre`, an exact power of two (layers whose values would leave
-// fp16's range).  A loop step covers the 32 channels of one 16-byte chunk index; it is not
+// A loop step covers the 32 channels of one 16-byte chunk index; it is not
 // unrolled: four copies of the step's code do not fit the instruction caches beside the other
 // roles'.
-template <int BK, int KM, int D, bool PRE>
-__device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, int w, int lane, uint32_t pre) {
+template <int BK, int KM, int D>
+__device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, int w, int lane) {
     constexpr int NJ = D / 32, PK = 16 / BK, KC = 4 * D * BK, W = BK / 2;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ps = smem_u32(part);
@@ -315,10 +327,6 @@ __device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, in
                 uint32_t a[4];
                 lds_words<4>(ps + KC + 16 * (4 * (2 * i + k1) + t), a);
                 s[k1][0] = a[0]; z[k1][0] = a[1]; s[k1][1] = a[2]; z[k1][1] = a[3];
-                if constexpr (PRE) {
-                    s[k1][0] = hmul2_bits(s[k1][0], pre); z[k1][0] = hmul2_bits(z[k1][0], pre);
-                    s[k1][1] = hmul2_bits(s[k1][1], pre); z[k1][1] = hmul2_bits(z[k1][1], pre);
-                }
             }
         }
 #pragma unroll
@@ -328,7 +336,6 @@ __device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, in
                 const uint8_t *a = part + KC + quant::tok_sz_off(8 * n + g, i, NJ);
                 st = *reinterpret_cast<const uint16_t *>(a) * 0x10001u;
                 zt = *reinterpret_cast<const uint16_t *>(a + 4 * NJ) * 0x10001u;
-                if constexpr (PRE) { st = hmul2_bits(st, pre); zt = hmul2_bits(zt, pre); }
             }
             uint32_t o[4];
 #pragma unroll
@@ -347,8 +354,8 @@ __device__ __forceinline__ void unpack_keys(const uint8_t *part, uint8_t *kt, in
 
 // Value block w of a tile -> fp16 columns of the V operand ([channel][token]); tokens from
 // `valid` on become zeros.  A loop step covers one 32-channel group.
-template <int BV, int D, bool PRE>
-__device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, int w, int lane, int valid, uint32_t pre) {
+template <int BV, int D>
+__device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, int w, int lane, int valid) {
     constexpr int NJ = D / 32, PV = 16 / BV, VC = 4 * D * BV, W = BV / 2;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ps = smem_u32(part);
@@ -372,10 +379,6 @@ __device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, 
                 z[n] &= m;
             }
         }
-        if constexpr (PRE) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) { s[n] = hmul2_bits(s[n], pre); z[n] = hmul2_bits(z[n], pre); }
-        }
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -391,19 +394,18 @@ __device__ __forceinline__ void unpack_values(const uint8_t *part, uint8_t *vt, 
     }
 }
 
-// The unpackers by bit width; layers that need `pre` take a path of their own.
-template <int KM, int D, bool PRE>
-__device__ __forceinline__ void unpack_keys_bits(int bits, const uint8_t *part, uint8_t *kt, int w, int lane, uint32_t pre) {
-    if (bits == 8) unpack_keys<8, KM, D, PRE>(part, kt, w, lane, pre);
-    else if (bits == 4) unpack_keys<4, KM, D, PRE>(part, kt, w, lane, pre);
-    else unpack_keys<2, KM, D, PRE>(part, kt, w, lane, pre);
+// The unpackers by bit width.
+template <int KM, int D>
+__device__ __forceinline__ void unpack_keys_bits(int bits, const uint8_t *part, uint8_t *kt, int w, int lane) {
+    if (bits == 8) unpack_keys<8, KM, D>(part, kt, w, lane);
+    else if (bits == 4) unpack_keys<4, KM, D>(part, kt, w, lane);
+    else unpack_keys<2, KM, D>(part, kt, w, lane);
 }
-template <int D, bool PRE>
-__device__ __forceinline__ void unpack_values_bits(int bits, const uint8_t *part, uint8_t *vt, int w, int lane, int valid,
-                                                   uint32_t pre) {
-    if (bits == 8) unpack_values<8, D, PRE>(part, vt, w, lane, valid, pre);
-    else if (bits == 4) unpack_values<4, D, PRE>(part, vt, w, lane, valid, pre);
-    else unpack_values<2, D, PRE>(part, vt, w, lane, valid, pre);
+template <int D>
+__device__ __forceinline__ void unpack_values_bits(int bits, const uint8_t *part, uint8_t *vt, int w, int lane, int valid) {
+    if (bits == 8) unpack_values<8, D>(part, vt, w, lane, valid);
+    else if (bits == 4) unpack_values<4, D>(part, vt, w, lane, valid);
+    else unpack_values<2, D>(part, vt, w, lane, valid);
 }
 
 // Byte offset of channel chunk c8 (8 channels d = 8 c8 ..) of `row` in a K-major operand whose
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     if (nrow <= 0) return;
     const int Hq = p.Hkv * p.G;
     const long long unit = static_cast<long long>(b) * p.Hkv + h;
-    const unsigned smax_k = p.smax[0], smax_v = p.smax[1];
+    const unsigned top_k = p.top[0], top_v = p.top[1];
     const int *depth = p.depth ? p.depth + static_cast<long long>(b) * p.T : nullptr;
     auto row_t = [&](int r) { return p.gmul ? static_cast<int>(__umulhi(row0 + r, p.gmul)) : row0 + r; };   // / G
 
@@ -536,14 +538,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
     const int n = te - tb;
     Waiter wait;
 
-    // exact power of two that keeps the layer's cached values inside fp16 (1 for any layer whose
-    // scales are below 2^14 / (2^b - 1))
-    auto pre_exp = [&](unsigned smax, int bits) {
-        const float sm = __half2float(__ushort_as_half(static_cast<unsigned short>(smax)));
-        const float top = sm * static_cast<float>((1 << bits) - 1);
-        return top >= 16384.f ? min(14, floor_log2(top) - 13) : 0;
-    };
-    const int ek = pre_exp(smax_k, p.bk), ev = pre_exp(smax_v, p.bv);
+    // exponent of the power of two that the layer's cached values are divided by: 0 unless a group's
+    // bound is above fp16's range (finite scales and zeros: below 2^24 + 2^16, so 10 at most)
+    auto pre_exp = [](unsigned top) { return top ? min(10, floor_log2(__uint_as_float(top)) - 14) : 0; };
+    const int ek = pre_exp(top_k), ev = pre_exp(top_v);
 
     // packed parts: first block and number of blocks of tile tb + i (the open group has packed
     // values only); bytes, ring
@@ -570,7 +568,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const int stages = is_v ? p.dv : p.dk;
         const uint8_t *ring = ring_of(is_v) + w * part_bytes;
         const uint32_t on = elect_one();
-        const uint32_t pre = (is_v ? ev : ek) ? h2_bits(__float2half2_rn(pow2f(-(is_v ? ev : ek)))) : 0u;
+        const int ex = is_v ? ev : ek;
         int st = 0, ph = 0;        // the next part's stage and phase (tiles without a part use none)
         for (int i = 0; i < n; ++i) {
             int buf, used;
@@ -584,16 +582,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             if (nb > 0) wait(&bar->part_full[is_v][st], ph);
             if (used > 0) wait(&bar->free[buf], (used - 1) & 1);
             const uint8_t *part = ring + st * 4 * part_bytes;
+            if (ex != 0 && has) scale_part<D>(smem_u32(part) + part_bytes - 4 * D, lane, pow2f(-ex));
             const bool is_open = tb + i < n_open;
             const int j0 = kTile * (tb + i) + 32 * w - pad;   // open tiles: the block's first drafted token
             if (!is_v && has) {
-                if (p.kmode == 0) {
-                    if (pre) unpack_keys_bits<0, D, true>(bits, part, tile, w, lane, pre);
-                    else unpack_keys_bits<0, D, false>(bits, part, tile, w, lane, pre);
-                } else {
-                    if (pre) unpack_keys_bits<1, D, true>(bits, part, tile, w, lane, pre);
-                    else unpack_keys_bits<1, D, false>(bits, part, tile, w, lane, pre);
-                }
+                if (p.kmode == 0) unpack_keys_bits<0, D>(bits, part, tile, w, lane);
+                else unpack_keys_bits<1, D>(bits, part, tile, w, lane);
             } else if (!is_v && is_open) {
                 // bf16 rows: the open group's, or drafted tokens (rows behind them are masked)
                 float *ksc = reinterpret_cast<float *>(smem + SM::kscale) + (i & 3) * kTile;
@@ -623,8 +617,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                         j0 < 0 ? (L & ~31) + lane : (lane < rows ? L + (depth ? depth[j0 + lane] : j0 + lane) : 0);
             } else if (is_v && has) {
                 const int valid = min(32, L - 32 * blk);
-                if (pre) unpack_values_bits<D, true>(bits, part, tile, w, lane, valid, pre);
-                else unpack_values_bits<D, false>(bits, part, tile, w, lane, valid, pre);
+                unpack_values_bits<D>(bits, part, tile, w, lane, valid);
             } else if (is_v && is_open && j0 < nk) {
                 // drafted values: token pairs (u, u + 1) of the block
                 const float fs = pow2f(-ev);

@@ -3,12 +3,16 @@ key by key, for tests that have to see small faults; and inputs whose result cou
 that a row sees.
 
 The bound.  Let w_i = exp(s_i) / sum exp(s), o = sum w_i v_i.  If score i is off by at most
-ds_i and the weight's rounding by a factor 1 +- e, then with r_i = exp(ds_i) (1 + e) - 1
+ds_i and the weight's rounding by a factor 1 +- e, then
 
-    |o' - o| <= sum w_i r_i |v_i - o| / (1 - sum w_i r_i)  +  (sum w_i (1 + r_i) dv_i) / (1 - ..)
+    |o' - o| <= (sum w_i r_i |v_i - o|  +  sum w_i (1 + r_i) (e |v_i| + dv_i)) / (1 - sum w_i r_i)
 
-(the weights' errors enter only times v_i - o: a common factor cancels), dv_i being the error of
-value i.  What ds, e and dv are is stated per kernel in `attention`."""
+with r_i = exp(ds_i) - 1 and dv_i the error of value i.  Proof: the kernels sum the weights before
+they are rounded, so o' = sum W_i (1 + E_i) (v_i + D_i) / sum W_i with W_i = w_i (1 + R_i), |R_i| <=
+r_i, |E_i| <= e, |D_i| <= dv_i.  Then o' - o = sum W_i (v_i - o) / sum W_i + sum W_i (E_i v_i + (1 +
+E_i) D_i) / sum W_i; as sum w_i (v_i - o) = 0, the first numerator is sum w_i R_i (v_i - o) (a common
+factor of the scores' errors cancels, the rounding of the weights does not), and sum W_i >= 1 - sum
+w_i r_i.  What ds, e and dv are is stated per kernel in `attention`."""
 import numpy as np
 
 H = 2.0 ** -11      # half a step of fp16, relative
@@ -19,12 +23,12 @@ def tanh_cap(s, cap):
 
 
 def attention(q, K, V, see, pos_q, pos_k, G, cap=0.0, alibi=None, window=0, scale=0.0, operands="fp16", kmax=None,
-              vmax=None, vstep=0.0):
+              vmax=None, vstep=0.0, kstep=0.0):
     """q [t, Hq, D], K, V [Hkv, n, D], see bool [t, n], positions [t], [n] -> (out, bound) [t, Hq, D].
 
     operands "fp16" (kvq_tree_attn): keys, values and weights are rounded to fp16, H of themselves
-    at most, values to a step of vstep (absolute, half a step) if that is coarser; a query or bf16
-    key row is exact to 2^-38 of its largest.  Scores: fp32 sums of D products, accumulated by the
+    at most, keys and values by kstep and vstep (absolute) if that is more; a query or bf16 key row
+    is exact to 2^-38 of its largest.  Scores: fp32 sums of D products, accumulated by the
     tensor cores: 2^-19 of the sum of the products' sizes.
     operands "fp32" (kvq_decode_attn_scored): a key is code * s + z, its two parts in products of
     their own whose factors carry 22 bits (hi and lo fp16), summed in fp32: 2^-19 of the parts'
@@ -49,7 +53,7 @@ def attention(q, K, V, see, pos_q, pos_k, G, cap=0.0, alibi=None, window=0, scal
             aq, ak = np.abs(q[r, h]), np.abs(k)
             s = (k @ q[r, h]) * scale
             if fp16:
-                ds = (H + 2.0 ** -19) * (ak @ aq) + 2.0 ** -38 * (aq.max() * ak.sum(1) + aq.sum() * ak.max(1))
+                ds = (np.maximum(H * ak, kstep) + 2.0 ** -19 * ak) @ aq + 2.0 ** -38 * (aq.max() * ak.sum(1) + aq.sum() * ak.max(1))
                 dv = np.maximum(H * np.abs(v), vstep)
             else:
                 ds = np.full(len(on), 2.0 ** -19 * 3 * (aq @ kmax[h // G]))
@@ -66,10 +70,10 @@ def attention(q, K, V, see, pos_q, pos_k, G, cap=0.0, alibi=None, window=0, scal
             w = np.exp(s - s.max())
             w /= w.sum()
             o = w @ v
-            f = w * (np.exp(ds) * (1 + e) - 1)
+            f = w * (np.exp(ds) - 1)
             left = max(1 - f.sum(), 0.1)
             out[r, h] = o
-            bound[r, h] = (f @ np.abs(v - o) + (w + f) @ dv) / left + 2.0 ** -22 * np.abs(o)
+            bound[r, h] = (f @ np.abs(v - o) + (w + f) @ (e * np.abs(v) + (1 + e) * dv)) / left + 2.0 ** -22 * np.abs(o)
     return out, bound
 
 
