@@ -389,8 +389,9 @@ typedef struct {
  * a row does not see has no influence on it, whatever K and V hold there.  Depths are >= 0,
  * positions below 2^31.
  * Accuracy: cached keys and values, drafted values and the softmax weights enter the products
- * rounded to fp16 (2^-11 of each at most); scores, softmax and sums are fp32.  Drafted values
- * beyond 65504 saturate there, unless infinite.  A layer with a group whose |zero| + scale
+ * rounded to fp16 (2^-11 of each at most; small weights 2^-32 of the row's largest, small drafted
+ * values 2^-20 of the largest drafted or open-group value of their request and kv head, or 2^-25,
+ * the lesser of the two); scores, softmax and sums are fp32.  Drafted values beyond 65504 saturate there, unless infinite.  A layer with a group whose |zero| + scale
  * (2^b - 1) is above 65504 is computed scaled by 2^-e to fp16's range (e <= 10): its values are then
  * off by up to 2^(e + b - 25) instead, if that is more.  T <= 4096.  workspace: device memory of
  * kvq_tree_attn_workspace_bytes, 256-byte aligned, owned by the call until it has run.

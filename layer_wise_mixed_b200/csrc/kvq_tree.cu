@@ -47,10 +47,13 @@
 // the step there).  Query rows and bf16 key rows are scaled by a power of two to below 2^15
 // (exact in fp16 to 2^-38 of the row's largest); layers with a value that would leave fp16's
 // range are scaled down as a whole, by 2^e (e = 1 .. 10; a scale or zero below 2^(e-14) is then
-// off by 2^(e-25), so a value by 2^(e+b-25) at most).  Weights are fp16 of 2^(s - m + 7): m
-// follows the running maximum, and lags by up to 2^8 so that the sums in tensor memory are
-// rescaled only when it grew by more; l sums them before that rounding.  Scores, m, l and O are
-// fp32.
+// off by 2^(e-25), so a value by 2^(e+b-25) at most).  Weights are fp16 of 2^(s - m + 7), off by
+// 2^-11 (subnormal ones by 2^-32 of the row's largest): m follows the running maximum, and lags
+// by up to 2^8 so that the sums in tensor memory are rescaled only when it grew by more; l sums
+// them before that rounding.  Scores, m, l and O are fp32.  Drafted values have the whole range
+// of bf16, and small ones would be fp16 subnormals or zero: a split's open tiles have an exponent
+// of their own (value_exp), and O goes from their unit to the packed tiles' as it does when m
+// grows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -225,8 +228,10 @@ __device__ __forceinline__ void operand_buffer(int v, int i, int &buf, int &use)
 struct TreeBars {
     uint64_t q_full, full[4], free[4], s_full[2], p_full[2], o_full[2];
     uint64_t part_full[2][4], part_free[2][4];   // packed parts (keys, values), per stage
+    uint64_t v_ready;      // open_top is final
     uint32_t tmem, bad_value;
     int min_pos;
+    uint32_t open_top;     // largest finite |value| of the split's open tiles (float bits; see value_exp)
 };
 static_assert(sizeof(TreeBars) <= 512, "barrier area");
 
@@ -443,6 +448,16 @@ __device__ __forceinline__ float store_scaled_row(uint8_t *tile, int row, int c8
     return pow2f(e - 14);
 }
 
+// Exponent e of the power of two that the values of a split's open tiles are divided by, from their
+// largest magnitude: the packed tiles' ev unless that is below 2^(ev - 3), else the one that brings
+// it to [2^14, 2^15).  So a value is off by 2^-11 of itself or 2^-22 of the largest, whichever is
+// more, and values of ordinary size share the packed tiles' exponent (no rescale between them).
+constexpr int kMinValueExp = -112;   // (2^-e stays a normal number)
+__device__ __forceinline__ int value_exp(uint32_t top_bits, int ev) {
+    const float top = __uint_as_float(top_bits);
+    return top >= pow2f(ev - 3) ? ev : max(kMinValueExp, floor_log2(top) - 14);   // (0: the least)
+}
+
 // Bounded waits; after one expiry no wait waits again.  The clock is read only after many
 // polls: reading the global timer takes longer than most of these waits.
 struct Waiter {
@@ -500,6 +515,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         } else {
             bar->bad_value = 0;
             bar->min_pos = 0x7FFFFFFF;
+            bar->open_top = 0;
+            mbar_init(&bar->v_ready, 4);
         }
         fence_mbar_init();
     }
@@ -568,7 +585,42 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
         const int stages = is_v ? p.dv : p.dk;
         const uint8_t *ring = ring_of(is_v) + w * part_bytes;
         const uint32_t on = elect_one();
-        const int ex = is_v ? ev : ek;
+        int vexp = ev;             // exponent of the open tiles' values
+        if (is_v && tb < n_open) {
+            // Largest finite magnitude of the split's drafted values and of the open group's.  A warp
+            // stops at the first value that leaves the exponent at ev: for ordinary values after one
+            // load.
+            const int ja = max(0, kTile * tb - pad), je = min(nk, kTile * min(te, n_open) - pad);
+            const uint4 *v = reinterpret_cast<const uint4 *>(p.vd + (unit * p.T + ja) * D);
+            const float enough = pow2f(ev - 3);
+            float top = 0.f;
+            for (int it = 32 * w + lane, end = (je - ja) * NL; it - lane < end; it += 128) {
+                const uint4 x = it < end ? v[it] : make_uint4(0u, 0u, 0u, 0u);
+                const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float a = fabsf(__uint_as_float(k & 1 ? xw[k >> 1] & 0xFFFF0000u : xw[k >> 1] << 16));
+                    if (a < INFINITY) top = fmaxf(top, a);
+                }
+                if (__any_sync(0xffffffffu, top >= enough)) break;
+            }
+            if (w == 0 && pad && tb == 0 && !__any_sync(0xffffffffu, top >= enough)) {
+                // the open group's packed values: a bound, |zero| + scale (2^b - 1), per token
+                const uint8_t *sz = p.rec + (rec_index(p.btab, b, p.Hkv, h, p.cap_blk, L >> 5) + 1) * (key_part + value_part) - 4 * D;
+                for (int j = 0; lane < open && j < NL / 4; ++j) {
+                    const uint8_t *a = sz + quant::tok_sz_off(lane, j, NL / 4);
+                    const float sc = __half2float(*reinterpret_cast<const __half *>(a));
+                    const float ze = __half2float(*reinterpret_cast<const __half *>(a + NL));
+                    top = fmaxf(top, fmaf(sc, static_cast<float>((1 << bits) - 1), fabsf(ze)));
+                }
+            }
+            const uint32_t wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            if (on) atomicMax(&bar->open_top, wtop);
+            __syncwarp();
+            arrive_one(on, &bar->v_ready);
+            wait(&bar->v_ready, 0);
+            vexp = value_exp(bar->open_top, ev);
+        }
         int st = 0, ph = 0;        // the next part's stage and phase (tiles without a part use none)
         for (int i = 0; i < n; ++i) {
             int buf, used;
@@ -582,8 +634,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             if (nb > 0) wait(&bar->part_full[is_v][st], ph);
             if (used > 0) wait(&bar->free[buf], (used - 1) & 1);
             const uint8_t *part = ring + st * 4 * part_bytes;
-            if (ex != 0 && has) scale_part<D>(smem_u32(part) + part_bytes - 4 * D, lane, pow2f(-ex));
             const bool is_open = tb + i < n_open;
+            const int ex = !is_v ? ek : (is_open ? vexp : ev);
+            if (ex != 0 && has) scale_part<D>(smem_u32(part) + part_bytes - 4 * D, lane, pow2f(-ex));
             const int j0 = kTile * (tb + i) + 32 * w - pad;   // open tiles: the block's first drafted token
             if (!is_v && has) {
                 if (p.kmode == 0) unpack_keys_bits<0, D>(bits, part, tile, w, lane);
@@ -620,7 +673,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 unpack_values_bits<D>(bits, part, tile, w, lane, valid);
             } else if (is_v && is_open && j0 < nk) {
                 // drafted values: token pairs (u, u + 1) of the block
-                const float fs = pow2f(-ev);
+                const float fs = pow2f(-vexp);
                 bool bad = false;
                 for (int it = lane; it < 16 * NL; it += 32) {
                     const int u = 2 * (it % 16), c = 8 * (it / 16), col = tile_col(w, u);
@@ -795,6 +848,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             __syncwarp();
             arrive_one(on, &bar->q_full);
         }
+        // exponent of the open tiles' values (final once the slot's first open tile's values are there)
+        auto open_exp = [&]() { return value_exp(bar->open_top, ev); };
         float m = -INFINITY, l = 0.f, rs = 0.f;
         const int first = TWO ? 0 : j, step = TWO ? 1 : 2;
         int use = 0;
@@ -932,20 +987,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
                 for (int c = H; c < NC; ++c) mx = top(x[c], mx);
                 const float f = shaped ? 1.f : rs;
                 // the maximum (in log2 units) moves only when it grew by more than the lag, then O and l
-                // are rescaled
+                // are rescaled; O also from the open tiles' unit to the packed ones' (never smaller)
                 mx *= f;
-                if (__any_sync(0xffffffffu, mx > m + kLag)) {
+                int shift = 0;   // at the slot's first packed tile
+                if (ti >= 0 && ti < step && use > 0) shift = open_exp() - ev;
+                if (__any_sync(0xffffffffu, mx > m + kLag) || shift != 0) {
                     const float mn = fmaxf(m, mx);
                     if (use > 0) {
                         const float al = m == -INFINITY ? 0.f : fast_exp2(m - mn);
                         l *= al;
+                        const float ao = al * pow2f(shift);
 #pragma unroll 1
                         for (int c = 0; c < D / 16; ++c) {
                             uint32_t y[16];
                             ld16_issue(to + 16 * c, y);
                             ld16_wait(y);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * al);
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * ao);
                             st16(to + 16 * c, y);
                         }
                     }
@@ -1024,7 +1082,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
             m = M;
         }
         if (busy && any) {
-            own *= pow2f(ev) * (final_ ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+            own *= final_ ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            // O's unit: the slot's last tile's (a product of its own: own times it may leave fp32's range)
+            const int last = TWO || ((n ^ j) & 1) ? n - 1 : n - 2;
+            const float ounit = pow2f(tb + last < n_open ? open_exp() : ev);
             float *dst = rows_o + tid * SM::ROW;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -1034,8 +1095,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_kernel(const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4 *>(dst + 32 * c + e) =
-                        make_float4(__uint_as_float(x[e]) * own, __uint_as_float(x[e + 1]) * own,
-                                    __uint_as_float(x[e + 2]) * own, __uint_as_float(x[e + 3]) * own);
+                        make_float4(__uint_as_float(x[e]) * own * ounit, __uint_as_float(x[e + 1]) * own * ounit,
+                                    __uint_as_float(x[e + 2]) * own * ounit, __uint_as_float(x[e + 3]) * own * ounit);
             }
         }
         if (!final_ && r < nrow && copy == 0 && (TWO || j == 0))

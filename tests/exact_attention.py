@@ -12,7 +12,9 @@ they are rounded, so o' = sum W_i (1 + E_i) (v_i + D_i) / sum W_i with W_i = w_i
 r_i, |E_i| <= e, |D_i| <= dv_i.  Then o' - o = sum W_i (v_i - o) / sum W_i + sum W_i (E_i v_i + (1 +
 E_i) D_i) / sum W_i; as sum w_i (v_i - o) = 0, the first numerator is sum w_i R_i (v_i - o) (a common
 factor of the scores' errors cancels, the rounding of the weights does not), and sum W_i >= 1 - sum
-w_i r_i.  What ds, e and dv are is stated per kernel in `attention`."""
+w_i r_i.  A fp16 weight is 2^(s_i - m + 7), m at most the row's largest score, so below 2^-14 it is off
+by half a step of 2^-24, 2^-32 of the row's largest weight, instead: e w_i is at least that.  What ds,
+e and dv are is stated per kernel in `attention`."""
 import numpy as np
 
 H = 2.0 ** -11      # half a step of fp16, relative
@@ -27,7 +29,7 @@ def attention(q, K, V, see, pos_q, pos_k, G, cap=0.0, alibi=None, window=0, scal
     """q [t, Hq, D], K, V [Hkv, n, D], see bool [t, n], positions [t], [n] -> (out, bound) [t, Hq, D].
 
     operands "fp16" (kvq_tree_attn): keys, values and weights are rounded to fp16, H of themselves
-    at most, keys and values by kstep and vstep (absolute) if that is more; a query or bf16 key row
+    at most, keys and values by kstep and vstep (absolute; one number or [n]) if that is more; a query or bf16 key row
     is exact to 2^-38 of its largest.  Scores: fp32 sums of D products, accumulated by the
     tensor cores: 2^-19 of the sum of the products' sizes.
     operands "fp32" (kvq_decode_attn_scored): a key is code * s + z, its two parts in products of
@@ -54,7 +56,7 @@ def attention(q, K, V, see, pos_q, pos_k, G, cap=0.0, alibi=None, window=0, scal
             s = (k @ q[r, h]) * scale
             if fp16:
                 ds = (np.maximum(H * ak, kstep) + 2.0 ** -19 * ak) @ aq + 2.0 ** -38 * (aq.max() * ak.sum(1) + aq.sum() * ak.max(1))
-                dv = np.maximum(H * np.abs(v), vstep)
+                dv = np.maximum(H * np.abs(v), vstep if np.ndim(vstep) == 0 else vstep[on][:, None])
             else:
                 ds = np.full(len(on), 2.0 ** -19 * 3 * (aq @ kmax[h // G]))
                 dv = np.full(v.shape, 2.0 ** -19 * 3) * vmax[h // G]
@@ -73,7 +75,8 @@ def attention(q, K, V, see, pos_q, pos_k, G, cap=0.0, alibi=None, window=0, scal
             f = w * (np.exp(ds) - 1)
             left = max(1 - f.sum(), 0.1)
             out[r, h] = o
-            bound[r, h] = (f @ np.abs(v - o) + (w + f) @ (e * np.abs(v) + (1 + e) * dv)) / left + 2.0 ** -22 * np.abs(o)
+            ew = np.maximum(e * (w + f), 2.0 ** -32 * (w + f).max()) if fp16 else e * (w + f)
+            bound[r, h] = (f @ np.abs(v - o) + ew @ np.abs(v) + (w + f + ew) @ dv) / left + 2.0 ** -22 * np.abs(o)
     return out, bound
 
 
