@@ -247,7 +247,8 @@ KVQ_API int kvq_reset_sequences(kvq_handle *h, const int32_t *seqs, int n);
 
 /* Read and clear the device status word (synchronizes `stream`).  KVQ_EDEVICE if a
  * kernel reported a bounded wait that expired (bit 0) or a slot index outside its source
- * (bit 1, kvq_append_selected); *flags gets the raw bits. */
+ * (bit 1, kvq_append_selected); *flags gets the raw bits.  0 before the first launch that follows a
+ * bind. */
 KVQ_API int kvq_device_status(kvq_handle *h, void *stream, unsigned *flags);
 
 /* Decode attention without any caller-provided scratch: the same computation and

@@ -1388,6 +1388,10 @@ int kvq_device_status(kvq_handle *h, void *stream, unsigned *flags) {
     int rc = check_bound(h);
     if (rc) return rc;
     unsigned v = 0;
+    if (!h->status_clear) {   // no launch since the bind has cleared the word, nor could have set it
+        if (flags) *flags = 0;
+        return ok();
+    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemcpyAsync(&v, h->ws + h->status_off, sizeof v, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
