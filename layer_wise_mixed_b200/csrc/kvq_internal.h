@@ -57,6 +57,9 @@ constexpr int kMaxRagged = 64;      // requests whose per-request lengths travel
                                     // parameters; larger batches use a device table
 constexpr int kDecodeWarps = 4;     // warps per decode CTA
 
+// SMs of a B200, for plans made without asking the device (workspaces are sized on hosts without one).
+constexpr int kSms = 148;
+
 // Device status word bits (written with atomicOr, read by kvq_device_status).
 constexpr unsigned kStatusWaitExpired = 1u;   // a bounded mbarrier wait gave up
 constexpr unsigned kStatusBadIndex = 2u;      // kvq_append_selected met an index outside its source

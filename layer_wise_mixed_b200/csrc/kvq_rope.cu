@@ -41,12 +41,19 @@ __device__ __forceinline__ uint4 f32x8_to_bf16(const float *x) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A CTA takes tpc tokens: as many as its threads hold, eight on long prompts, where the next
-// pass's rows are fetched before this pass's are written.  Measured on 16,384 tokens of 48 rows
-// of 128 channels (403 MB): 92 us, 4.4 TB/s, 67% of the measured copy rate; one token per CTA 99-105
-// us; a persistent grid that fetched across tokens 140 us (78 registers: fewer threads in
-// flight).  A decode step's 64 tokens are bound by the launch.  Dynamic shared memory: tpc *
-// rot / 2 (cos, sin) pairs.
+// A CTA takes tpc tokens: as many as its threads hold, or more (4, 8 or 16: fewer barriers and angle
+// steps per token, the next pass's rows fetched before this pass's are written) where the launch
+// then still has six CTAs per SM, two rounds of the three that an SM holds.  Device time in us with
+// 1 (as many as fit) / 4 / 8 / 16 tokens per CTA, 48 rows of 128 channels (Llama heads):
+//   tokens   2,048: 16.4 / 16.9 / 22.0 / 21.3      8,192: 54.3 / 51.2 / 51.2 / 58.2
+//            4,096: 29.2 / 27.1 / 30.7 / 39.9     12,000: 76.8 / 72.7 / 74.8 / 79.9
+//           16,384: 101.4 / 94.2 / 93.2 / 93.2    65,536: 386 / 354 / 350 / 344 (72% of the copy rate)
+// 36 rows (28 + 8 heads): 4,096 tokens 22.2 / 21.9 / 24.2 / 31.7, 16,384 tokens 77.9 / 76.8 / 73.7 /
+// 73.8.  10 rows (4 tokens fit): 8,192 tokens 16.4 with 4, 16.8 with 8, the rule's worst of those
+// measured.  Two tokens where one fits lose up to 26% (half-empty second passes).  A persistent
+// grid that fetched across tokens: 140 us at 16,384 (78 registers: fewer threads in flight).  What
+// bounds a long prompt: loads in flight; a decode step's 64 tokens: the launch.  Dynamic shared
+// memory: tpc * rot / 2 (cos, sin) pairs.
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams p, int tpc) {
     pdl_enter();
@@ -172,7 +179,8 @@ cudaError_t launch_rope(const RopeParams &p, cudaStream_t st) {
     int tpc = kRopeThreads / (rows * tpr);
     if (tpc < 1) tpc = 1;
     if (tpc > 16) tpc = 16;
-    if (tokens >= 16 * 1024) tpc = tpc < 8 ? 8 : tpc;   // long prompts: fewer barriers and angle steps per token
+    for (int t = 16; t >= 4; t /= 2)   // (measured: see rope_kernel)
+        if (t > tpc && tokens >= 6LL * kSms * t) tpc = t;
     if (tokens < tpc) tpc = static_cast<int>(tokens);
     const int want = (tpc * rows * tpr + 31) / 32 * 32;
     const int threads = want < kRopeThreads ? want : kRopeThreads;

@@ -1219,12 +1219,10 @@ bool g_tree_set[64][8];   // per device ordinal: shared-memory limits raised
 
 int tree_row_groups(int rows) { return (rows + 255) / 256; }
 
-constexpr int kTreeSms = 148;
-
 // Partials are sized for at most four CTAs per SM.
 int tree_max_splits(int B, int Hkv, int rows) {
     const long long ctas = static_cast<long long>(B) * Hkv * tree_row_groups(rows);
-    return static_cast<int>(std::max(1LL, std::min(64LL, 4LL * kTreeSms / ctas)));
+    return static_cast<int>(std::max(1LL, std::min(64LL, 4LL * kSms / ctas)));
 }
 
 int tree_splits(int B, int Hkv, int row_groups, long long tiles, int max_splits) {
@@ -1232,7 +1230,7 @@ int tree_splits(int B, int Hkv, int row_groups, long long tiles, int max_splits)
     double best = 1e300;
     int S = 1;
     for (int s = 1; s <= max_splits && s <= tiles; ++s) {
-        const double waves = static_cast<double>((ctas * s + kTreeSms - 1) / kTreeSms);
+        const double waves = static_cast<double>((ctas * s + kSms - 1) / kSms);
         const double cost = waves * (static_cast<double>((tiles + s - 1) / s) + 4.0) + (s > 1 ? 2.0 : 0.0);
         if (cost < best - 1e-9) {
             best = cost;
