@@ -26,10 +26,11 @@ __device__ __forceinline__ void group_params(float mn, float mx, int bits, float
 }
 
 // Float bits of a group's value bound if it is above fp16's range (non-negative floats order like
-// their bits), else 0.
+// their bits), else 0.  Groups whose scale or zero is not finite do not count: no scaling helps them,
+// and the layer's other groups would lose bits to it.
 __device__ __forceinline__ unsigned group_top(float s, float z, int bits) {
     const float top = fmaf(s, static_cast<float>((1 << bits) - 1), fabsf(z));
-    return top > kHalfMax ? __float_as_uint(top) : 0u;
+    return top > kHalfMax && top < INFINITY ? __float_as_uint(top) : 0u;
 }
 
 __device__ __forceinline__ int group_code(float x, float s, float z, int bits) {
