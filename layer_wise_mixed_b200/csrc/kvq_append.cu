@@ -92,7 +92,7 @@ __device__ void per_token_half(const AppendParams &p, int role, int unit, int hb
                 const int so = tok_sz_off(u, j, nj);
                 *reinterpret_cast<uint16_t *>(sz + so) = s16;
                 *reinterpret_cast<uint16_t *>(sz + so + 4 * nj) = z16;
-                atomicMax(cta_smax, static_cast<unsigned>(s16));
+                atomicMax(cta_smax, scale_top(s16));
                 if (const unsigned top = group_top(s, z, bits)) atomicMax(cta_top, top);
             }
         }
@@ -151,7 +151,7 @@ __device__ void per_channel_group(const AppendParams &p, int unit, int q, bool d
             const int so = chan_sz_off(d);
             *reinterpret_cast<uint16_t *>(rec + p.kc + so) = s16;
             *reinterpret_cast<uint16_t *>(rec + p.kc + so + 4) = z16;
-            atomicMax(cta_smax, static_cast<unsigned>(s16));
+            atomicMax(cta_smax, scale_top(s16));
             if (const unsigned top = group_top(s, z, p.bk)) atomicMax(cta_top, top);
         }
         __syncthreads();

@@ -845,7 +845,7 @@ __device__ __forceinline__ void append_token_quantize(uint8_t *scratch, const ui
             szs[(role * NJ + j) * 2] = s16;
             szs[(role * NJ + j) * 2 + 1] = z16;
         }
-        smax_new[role] = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(s16));
+        smax_new[role] = __reduce_max_sync(0xffffffffu, quant::scale_top(s16));
         top_new[role] = __reduce_max_sync(0xffffffffu, quant::group_top(sc, z, bits));
     }
     __syncwarp();

@@ -69,7 +69,7 @@ __device__ __forceinline__ void quant_token_row(const uint16_t *row, int bits, u
             const int so = tok_sz_off(u, j, kNJ);
             *reinterpret_cast<uint16_t *>(sz + so) = s16;
             *reinterpret_cast<uint16_t *>(sz + so + 4 * kNJ) = z16;
-            atomicMax(smax_cta, static_cast<unsigned>(s16));
+            atomicMax(smax_cta, scale_top(s16));
         }
     }
 }
@@ -145,7 +145,7 @@ __device__ void write_int2_group(uint8_t *rec, SrcFn src_row, float (*xs)[kD], u
         const int so = chan_sz_off(d);
         *reinterpret_cast<uint16_t *>(rec + KC + so) = s16;
         *reinterpret_cast<uint16_t *>(rec + KC + so + 4) = z16;
-        atomicMax(smax_k, static_cast<unsigned>(s16));
+        atomicMax(smax_k, scale_top(s16));
     }
     const int warp = threadIdx.x >> 5;
     for (int u = warp; u < 32; u += kWarps) {

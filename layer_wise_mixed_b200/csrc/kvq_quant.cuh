@@ -25,6 +25,11 @@ __device__ __forceinline__ void group_params(float mn, float mx, int bits, float
     z16 = __half_as_ushort(zh);
 }
 
+// A group's scale as it counts for its layer's maximum (fp16 bits): 0 if it is not finite.  The maximum
+// sets the decode kernels' fp16 operand scaling, so one infinite scale would cost every other request
+// its bits; the group itself is not finite with any scaling.
+__device__ __forceinline__ unsigned scale_top(uint16_t s16) { return s16 < 0x7C00u ? s16 : 0u; }
+
 // Float bits of a group's value bound if it is above fp16's range (non-negative floats order like
 // their bits), else 0.  Groups whose scale or zero is not finite do not count: no scaling helps them,
 // and the layer's other groups would lose bits to it.
