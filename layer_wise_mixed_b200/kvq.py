@@ -147,10 +147,12 @@ def _stream(stream) -> Optional[int]:
 
 
 def _torch_stream(stream, device):
-    """The torch stream of a Stream object or of a raw handle on `device`."""
+    """The torch stream of a stream object or of a raw handle on `device`."""
     import torch
-    if not isinstance(stream, int):
+    if isinstance(stream, torch.cuda.Stream):
         return stream
+    if not isinstance(stream, int):
+        stream = stream.cuda_stream   # (another library's stream object)
     if stream in (0, 1):   # the legacy default stream's two handles
         return torch.cuda.default_stream(device)
     return torch.cuda.ExternalStream(stream, device=device)

@@ -98,3 +98,15 @@ def test_append_on_another_stream():
     torch.cuda.current_stream().wait_stream(side)
     other.append_selected(0, Kd, Vd, index, [3, 2])
     assert np.array_equal(cache.export_layer(0), other.export_layer(0))
+
+
+def test_a_stream_object_of_another_library():
+    """Any object that holds the handle as cuda_stream names a stream, as in the older calls."""
+    class Other:
+        cuda_stream = torch.cuda.Stream().cuda_stream
+    cache, q, Kd, Vd, _ = setup()
+    want = cache.tree_attn(0, q, Kd, Vd)
+    torch.cuda.synchronize()
+    got = cache.tree_attn(0, q, Kd, Vd, stream=Other())
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
