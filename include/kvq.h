@@ -339,8 +339,9 @@ KVQ_API int kvq_tag_allocate(int num_tags, const double *D2, const double *D4, c
  * handle share the bound workspace (batches above 64: the layer's length table; split
  * partials): order them on the GPU when they go to different streams.  The first call that
  * launches after kvq_bind also clears the library's words in the workspace and cannot be
- * captured into a graph (KVQ_EINVAL from kvq_tree_attn and kvq_append_selected).  kvq_tree_attn keeps
- * its partials and tables in the workspace passed to it. */
+ * captured into a graph (KVQ_EINVAL from kvq_tree_attn and kvq_append_selected).  A captured call
+ * keeps the lengths, counts and splits it was captured with.  kvq_tree_attn keeps its partials and
+ * tables in the workspace passed to it. */
 
 /* Norm and rotation of a projection's rows. */
 typedef struct {
@@ -368,9 +369,12 @@ KVQ_API int kvq_norm_rope(kvq_handle *h, int layer, const void *qkv, int64_t bat
 
 /* How scores become weights: s = scale * (q . k); capped s = softcap * tanh(s / softcap);
  * then s -= alibi[hq] * (position of q - position of k); a key is seen only if position of
- * q - position of k < window.  All-zero (or a NULL pointer to it): plain attention. */
+ * q - position of k < window.  All-zero (or a NULL pointer to it): plain attention.  Scores are
+ * fp32: a bias is off by 2^-21 of itself at most, a capped score by 2^-20 of a cap up to 64 and by
+ * 2^-18 of itself under a larger one.  Cached values are taken to be finite: a cached token whose
+ * value groups hold infinities may reach rows of its own request that a window hides it from. */
 typedef struct {
-    float softcap;         /* 0: none; else > 0, finite: off by 2^-20 of a cap up to 64, by 2^-18 of the score above */
+    float softcap;         /* 0: none; else > 0, finite */
     const float *alibi;    /* device fp32 [n_q_heads], or NULL */
     int window;            /* 0: none; else >= 1 */
     float scale;           /* 0: 1 / sqrt(head_dim) */
@@ -387,16 +391,19 @@ typedef struct {
  * NULL: T each): request b has its first n_draft[b] tokens; output rows from there on are
  * left as they were, and the values behind them in q, K, V and mask have no influence.
  * Requests may be empty (length 0).  A row that sees no key comes out as zeros; a key that
- * a row does not see has no influence on it, whatever K and V hold there.  Depths are >= 0,
- * positions below 2^31.
+ * a row does not see has no influence on it (but on the rounding of small values, below),
+ * whatever K and V hold there.  Depths are >= 0, positions below 2^31.
  * Accuracy: cached keys and values, drafted values and the softmax weights enter the products
- * rounded to fp16 (2^-11 of each at most; small weights 2^-32 of the row's largest, small drafted
- * values 2^-20 of the largest drafted or open-group value of their request and kv head, or 2^-25,
- * the lesser of the two); scores, softmax and sums are fp32.  Drafted values beyond 65504 saturate there, unless infinite.  A layer with a group whose |zero| + scale
- * (2^b - 1) is above 65504 is computed scaled by 2^-e to fp16's range (e <= 10): its values are then
- * off by up to 2^(e + b - 25) instead, if that is more.  T <= 4096.  workspace: device memory of
- * kvq_tree_attn_workspace_bytes, 256-byte aligned, owned by the call until it has run.
- * One launch, and a merge launch when the sequence is split. */
+ * rounded to fp16, 2^-11 of each at most, also with out_fp32 (kvq_decode_attn and
+ * kvq_decode_attn_scored carry 22 bits).  Small weights: 2^-32 of the row's largest.  Small
+ * drafted values: the lesser of 2^-25 and 2^-20 of the largest drafted or open-group value of
+ * their request and kv head.  Drafted values beyond 65504 saturate there, unless infinite.  A
+ * layer with a group whose |zero| + scale (2^b - 1) is above 65504 is computed scaled by 2^-e
+ * to fp16's range (e <= 10): its values are then off by up to 2^(e + b - 25), if that is more.
+ * Scores, softmax and sums are fp32.
+ * T <= 4096.  workspace: device memory of kvq_tree_attn_workspace_bytes, 256-byte aligned,
+ * owned by the call until it has run.  One launch, and a merge launch when the sequence is
+ * split. */
 KVQ_API int kvq_tree_attn(kvq_handle *h, int layer, const void *q, const void *K, const void *V, int T,
                           const int32_t *n_draft, const uint32_t *mask, const int32_t *depth,
                           const kvq_score_opts *opts, void *out, int out_fp32, void *workspace,

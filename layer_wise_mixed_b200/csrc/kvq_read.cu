@@ -3,7 +3,7 @@
 // value = code * scale + zero (the format's dequantisation; fp32 FMA, rounded once to bf16);
 // the open per-channel key group's bf16 keys are copied.  Bound: HBM, mostly the writes (a
 // token's K4V2 keys and values are 128 bytes packed and 512 bytes as bf16).  Measured: 8000 tokens of
-// 64 (request, kv head) units, K4V2, 64 us: 5.1 TB/s, 78% of the measured copy rate.
+// 64 (request, kv head) units, K4V2, 65.4 us: 5.0 TB/s, 77% of the measured copy rate.
 //
 // One warp per (unit, 32-token block).  A lane's packed words are contiguous (the storage
 // format's fragments), its codes belong to 8 tokens x D / 4 channel pairs; rows are put

@@ -52,8 +52,9 @@ __device__ __forceinline__ uint4 f32x8_to_bf16(const float *x) {
 // 73.8.  10 rows (4 tokens fit): 8,192 tokens 16.4 with 4, 16.8 with 8, the rule's worst of those
 // measured.  Two tokens where one fits lose up to 26% (half-empty second passes).  A persistent
 // grid that fetched across tokens: 140 us at 16,384 (78 registers: fewer threads in flight).  What
-// bounds a long prompt: loads in flight; a decode step's 64 tokens: the launch.  Dynamic shared
-// memory: tpc * rot / 2 (cos, sin) pairs.
+// bounds a long prompt: the L1 / shared-memory data path (80% of its wavefronts: a thread's angle pairs lie
+// 64 bytes apart from its neighbour's) and issue (74%); DRAM is at 44%.  A decode step's 64 tokens (2.9 us)
+// are bound by the launch.  Dynamic shared memory: tpc * rot / 2 (cos, sin) pairs.
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams p, int tpc) {
     pdl_enter();

@@ -31,16 +31,23 @@
 //   token u of block w: u = 16 kk + 8 ch + 2 t + hb   ->  64 (w / 2) + 16 t + 8 (w % 2) + 4 kk + 2 ch + hb
 //
 // Measured (Llama shape, 8 kv heads, 4 query heads each): 64 drafted tokens at batch 16, context
-// 32768, K4V4: 0.71 ms, 0.78 PFLOP/s, 46% of the measured bf16 rate; 16 drafted tokens at batch
-// 64, context 4096, K4V2: 213 us (padded to 128 rows, the MMAs alone would take 63 us, the bytes
-// 44 us).  What bounds it: the issue of the unpack and softmax warps.  The tensor pipe is active 29%
-// of the cycles, 46% of issue slots are used, and the stall that leads among warps that could
-// run is the instruction fetch (no_instruction, 1.7 cycles per issued instruction): four
-// roles share each scheduler's instruction cache.  Hence small loop bodies rather than unrolled
-// ones.  Measured and not kept: a second team of unpack warps (no gain, slower starts),
+// 32768, K4V4: 0.70 ms, 0.79 PFLOP/s, 47% of the measured bf16 rate; 16 drafted tokens at batch
+// 64, context 4096, K4V2: 214 us (padded to 128 rows, the MMAs alone would take 63 us, the bytes
+// 44 us).  What bounds it.  One row tile (64 rows): the issue of the unpack and softmax warps; the
+// tensor pipe is active 30% of the cycles, 47% of issue slots are used, and the stall that leads
+// among warps that could run is the instruction fetch (no_instruction, 1.4 cycles per issued
+// instruction): four roles share each scheduler's instruction cache, hence small loop bodies
+// rather than unrolled ones.  Two row tiles: 39% of issue slots, tensor pipe 27%, XU 27%, so no
+// pipe: the handshakes between the roles (waiting roles: 5.5 cycles per issue).  The grid adds to it:
+// one split count for all requests, so 128 CTAs leave 20 of 148 SMs idle, 512 take 3.46 waves, and a
+// ragged batch ends with its longest request.  A capped score costs two more special-function
+// operations (500-token chunks: 132 us capped, 98 us not).  A single short request (11 us, 9.5 us
+// with nothing cached): launch, a CTA's set-up, and one pass through the roles.  Registers: the four
+// instances without copies spill 64 to 100 bytes, those with two copies 8.
+// Measured and not kept: a second team of unpack warps (no gain, slower starts),
 // polynomial exponentials for part of a row (4-17% slower: more instructions), a single pass with
 // a lagging maximum (slower), four operand buffers with two row tiles (the copies' ring shrinks
-// to one stage).
+// to one stage), unpack loops of their own for open and packed tiles (2-10% slower single requests).
 //
 // Roundings.  A cached key or value is one fp16 FMA of its exact code: off by 2^-11 of itself
 // at most, and exact below fp16's normal numbers (code, scale and zero are whole multiples of
